@@ -127,8 +127,8 @@ def _weights(gen, experts, n, k):
 
 
 def _route(gen, rows, experts, top_k, zipf):
-    """Expert-sorted slots: token of each sorted slot, offsets per expert, and the experts
-    that have rows (ascending, then -1) with their count."""
+    """Expert-sorted slots: token of each sorted slot, offsets per expert, and the largest
+    number of rows an expert has."""
     u = torch.rand((rows, experts), generator=gen, device="cuda", dtype=torch.float64)
     logits = -torch.log(-torch.log(u.clamp(1e-300, 1.0 - 1e-16)))
     rank = torch.randperm(experts, generator=gen, device="cuda") + 1
@@ -137,11 +137,7 @@ def _route(gen, rows, experts, top_k, zipf):
     count = torch.bincount(ids, minlength=experts)
     offsets = torch.zeros(experts + 1, dtype=torch.int32, device="cuda")
     offsets[1:] = count.cumsum(0)
-    active = torch.full((experts,), -1, dtype=torch.int32, device="cuda")
-    used = torch.nonzero(count).view(-1)
-    active[:used.numel()] = used.int()
-    counters = torch.tensor([used.numel(), 0], dtype=torch.int32, device="cuda")
-    return (order // top_k).int(), offsets, active, counters, int(count.max())
+    return (order // top_k).int(), offsets, int(count.max())
 
 
 def prepare(case, seed):
@@ -165,9 +161,7 @@ def prepare(case, seed):
     else:
         experts, top_k = case["experts"], case["top_k"]
         rows = case["rows"] * top_k
-        tok, offsets, active, counters, most = _route(gen, case["rows"], experts, top_k,
-                                                      case["zipf"])
-        st.update(offsets=offsets, active=active, counters=counters, most=most, rows=rows)
+        tok, st["offsets"], st["most"] = _route(gen, case["rows"], experts, top_k, case["zipf"])
         # gate_up gathers token rows; the down projection reads one row per sorted slot
         st["gather"] = tok if swiglu else None
         st["a"], st["sa"] = _quantised_rows(gen, case["rows"] if swiglu else rows, k)
@@ -265,14 +259,11 @@ def _hip(st):
         hip.moe_dense_gate_up_swiglu_fp8(st["a"], st["sa"], st["w"][0], st["sw"][0], st["w"][1],
                                          st["sw"][1], st["q"], st["scale"], LIMIT)
         return [st["q"], st["scale"]]
-    listed_experts = {"active_experts": st["active"], "counters": st["counters"]}
     if op == "grouped":
-        hip.moe_w8a8_grouped_gemm(st["a"], st["sa"], st["table"], st["offsets"], st["c"],
-                                  **listed_experts)
+        hip.moe_w8a8_grouped_gemm(st["a"], st["sa"], st["table"], st["offsets"], st["c"])
         return [st["c"]]
     hip.moe_w8a8_grouped_gemm_swiglu(st["a"], st["sa"], st["table"], st["offsets"], st["q"],
-                                     st["scale"], LIMIT, a_gather=st["gather"],
-                                     **listed_experts)
+                                     st["scale"], LIMIT, a_gather=st["gather"])
     return [st["q"], st["scale"]]
 
 
