@@ -16,12 +16,16 @@ Calls (same names as the C ABI):
   GEMMs (gate/up with the SwiGLU in the epilogue, then down).
 - ``moe_row_union``, ``moe_w4a16_gemv_union``, ``moe_w4a16_gemv_union_swiglu``: the
   decode / verify path for a few rows (the union of their experts, each swept once).
+- ``moe_quant_fp8``, ``moe_w8a8_grouped_gemm``, ``moe_w8a8_grouped_gemm_swiglu``,
+  ``moe_dense_gemm_fp8``, ``moe_dense_gate_up_swiglu_fp8``: the layer and the shared expert on
+  E4M3 weights and activations with one FP32 scale per block of 128.
 
 Helpers: ``ExpertTable`` (device pointer table of per-expert NVFP4 weights),
 ``Workspace`` (every buffer of one layer call, allocated once), ``SharedExpert`` (the
 shared expert's weights and buffers), ``moe_layer`` (the calls of one routed layer in
 order), ``DecodeWorkspace`` and ``moe_layer_decode`` (the same layer for a few rows through
-the union path).
+the union path), and their FP8 counterparts ``Fp8ExpertTable``, ``Fp8Workspace``,
+``SharedExpertFp8`` and ``moe_layer_fp8``.
 """
 
 from __future__ import annotations
@@ -39,6 +43,9 @@ __all__ = [
     "moe_layer_decode", "UNION_MAX_ROWS", "source_sha256", "moe_hbm_read_probe",
     "moe_dense_gemm_bf16_noalloc", "DENSE_NOALLOC_SCRATCH_BYTES", "moe_dense_splitk_ways",
     "moe_dense_gemm_bf16_partials", "moe_combine_partials", "SharedPartials",
+    "moe_quant_fp8", "moe_dense_gemm_fp8", "moe_dense_gate_up_swiglu_fp8",
+    "moe_w8a8_grouped_gemm", "moe_w8a8_grouped_gemm_swiglu", "Fp8ExpertTable", "Fp8Workspace",
+    "SharedExpertFp8", "moe_layer_fp8", "FP8_MAX_K",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_w4a16.so")
@@ -52,13 +59,16 @@ EXPORTS = (
     "moe_dense_workspace_bytes", "moe_zero_rows", "moe_row_union", "moe_w4a16_gemv_union",
     "moe_w4a16_gemv_union_swiglu", "moe_hbm_read_probe", "moe_dense_gemm_bf16_noalloc",
     "moe_align_zero", "moe_dense_splitk_ways", "moe_dense_gemm_bf16_partials",
-    "moe_combine_partials",
+    "moe_combine_partials", "moe_quant_fp8", "moe_dense_gemm_fp8",
+    "moe_dense_gate_up_swiglu_fp8", "moe_w8a8_grouped_gemm", "moe_w8a8_grouped_gemm_swiglu",
 )
 
 UNION_MAX_IDS = 1024  # MOE_UNION_MAX_IDS: rows * top_k of moe_row_union
 UNION_MAX_ROWS = 16  # MOE_UNION_MAX_ROWS: rows of moe_w4a16_gemv_union
 UNION_GEMV_MAX_IDS = 512  # MOE_UNION_GEMV_MAX_IDS: rows * top_k of moe_w4a16_gemv_union
 DENSE_NOALLOC_SCRATCH_BYTES = 32 << 20  # MOE_DENSE_NOALLOC_SCRATCH_BYTES
+FP8_MAX_K = 32768  # MOE_FP8_MAX_K
+FP8_BLOCK = 128  # values per scale
 
 _LIB = None
 
@@ -108,6 +118,18 @@ _SIGNATURES = {
     "moe_w4a16_gemv_union_swiglu": (
         [_vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i64, _i32, _i32,
          _f32, _vp], ctypes.c_int),
+    "moe_quant_fp8": ([_vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _vp], ctypes.c_int),
+    "moe_dense_gemm_fp8": ([_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32,
+                            _vp], ctypes.c_int),
+    "moe_dense_gate_up_swiglu_fp8": (
+        [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _i32,
+         _f32, _vp], ctypes.c_int),
+    "moe_w8a8_grouped_gemm": (
+        [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp],
+        ctypes.c_int),
+    "moe_w8a8_grouped_gemm_swiglu": (
+        [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _i64, _i32, _i32,
+         _i32, _f32, _vp], ctypes.c_int),
 }
 
 
@@ -625,6 +647,164 @@ def moe_dense_gate_up_swiglu_bf16(a, gate_w, up_w, act, limit: float, stream=Non
         wp, wb, _stream(stream)))
 
 
+def _fp8_matrix(t, name):
+    """Leading dimension of a row-major 2-D device tensor of E4M3 codes."""
+    import torch
+
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"{name}: expected E4M3 codes (float8_e4m3fn or uint8), got {t.dtype}")
+    if t.dim() != 2 or t.stride(1) != 1 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a row-major 2-D device tensor")
+    return t.stride(0)
+
+
+def _scale_matrix(t, rows, cols, name, contiguous=False):
+    """Leading dimension of a float32 [rows, cols] device tensor (at least)."""
+    import torch
+
+    if t.dtype != torch.float32 or t.dim() != 2 or not t.is_cuda:
+        raise TypeError(f"{name}: expected a 2-D float32 device tensor")
+    if t.shape[0] < rows or t.shape[1] < cols or (cols > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: needs {rows} x {cols} scales, rows contiguous")
+    if contiguous and (t.shape[1] != cols or not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a contiguous [{rows}, {cols}] tensor")
+    # of a single row the stride says nothing
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+
+
+def _fp8_blocks(n):
+    return -(-n // FP8_BLOCK)
+
+
+def _same_device(*tensors):
+    """Raises unless every tensor lies on the current device (the launch goes there)."""
+    import torch
+
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor lies on {t.device}, the current device is cuda:{dev}")
+
+
+def moe_quant_fp8(x, q, scale, stream=None) -> None:
+    """Quantise BF16 rows ``x [rows, cols]`` to E4M3 codes ``q [rows, cols]`` with one FP32
+    scale per row and 128 columns, ``scale [rows, ceil(cols / 128)]``; see the header."""
+    x, ld_x = _bf16_matrix(x, "x")
+    ld_q = _fp8_matrix(q, "q")
+    rows, cols = x.shape
+    if tuple(q.shape) != (rows, cols):
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
+    ld_s = _scale_matrix(scale, rows, _fp8_blocks(cols), "scale")
+    _same_device(x, q, scale)
+    _check("moe_quant_fp8", load().moe_quant_fp8(
+        _p(x), ld_x, _p(q), ld_q, _p(scale), ld_s, rows, cols, _stream(stream)))
+
+
+def moe_dense_gemm_fp8(a, a_scale, b, b_scale, c, stream=None) -> None:
+    """``c[m, n] = (a * a_scale)[m, :] @ (b * b_scale)[n, :]`` for E4M3 ``a [M, K]`` with
+    ``a_scale [M, ceil(K / 128)]`` and ``b [N, K]`` with ``b_scale [ceil(N / 128),
+    ceil(K / 128)]``, BF16 ``c [M, N]``."""
+    lda, ldb = _fp8_matrix(a, "a"), _fp8_matrix(b, "b")
+    c, ldc = _bf16_matrix(c, "c")
+    m, k = a.shape
+    n = b.shape[0]
+    if b.shape[1] != k or tuple(c.shape) != (m, n):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, "
+                         f"c {tuple(c.shape)}")
+    kb = _fp8_blocks(k)
+    ld_as = _scale_matrix(a_scale, m, kb, "a_scale")
+    _scale_matrix(b_scale, _fp8_blocks(n), kb, "b_scale", contiguous=True)
+    _same_device(a, a_scale, b, b_scale, c)
+    _check("moe_dense_gemm_fp8", load().moe_dense_gemm_fp8(
+        _p(a), lda, _p(a_scale), ld_as, _p(b), ldb, _p(b_scale), _p(c), ldc, m, n, k,
+        _stream(stream)))
+
+
+def moe_dense_gate_up_swiglu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale, act, act_scale,
+                                 limit: float, stream=None) -> None:
+    """The shared expert's gate and up products (``gate_w``, ``up_w`` E4M3 ``[I, K]``, same
+    strides), the clamped SwiGLU and the quantisation of its output in one launch: E4M3
+    ``act [M, I]`` with ``act_scale [M, ceil(I / 128)]``."""
+    lda, ldw = _fp8_matrix(a, "a"), _fp8_matrix(gate_w, "gate_w")
+    ld_act = _fp8_matrix(act, "act")
+    if _fp8_matrix(up_w, "up_w") != ldw or up_w.shape != gate_w.shape:
+        raise ValueError("gate_w and up_w must have the same shape and strides")
+    m, k = a.shape
+    inter = gate_w.shape[0]
+    if gate_w.shape[1] != k or tuple(act.shape) != (m, inter):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, gate_w {tuple(gate_w.shape)}, "
+                         f"act {tuple(act.shape)}")
+    kb, ib = _fp8_blocks(k), _fp8_blocks(inter)
+    ld_as = _scale_matrix(a_scale, m, kb, "a_scale")
+    _scale_matrix(gate_scale, ib, kb, "gate_scale", contiguous=True)
+    _scale_matrix(up_scale, ib, kb, "up_scale", contiguous=True)
+    ld_os = _scale_matrix(act_scale, m, ib, "act_scale")
+    _same_device(a, a_scale, gate_w, gate_scale, up_w, up_scale, act, act_scale)
+    _check("moe_dense_gate_up_swiglu_fp8", load().moe_dense_gate_up_swiglu_fp8(
+        _p(a), lda, _p(a_scale), ld_as, _p(gate_w), _p(gate_scale), _p(up_w), _p(up_scale), ldw,
+        _p(act), ld_act, _p(act_scale), ld_os, m, inter, k, float(limit), _stream(stream)))
+
+
+def _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows, out_rows):
+    """Checks the row side of a grouped FP8 call; (lda, ld_a_scale, rows)."""
+    import torch
+
+    lda = _fp8_matrix(a, "a")
+    _want(expert_offsets, torch.int32, "expert_offsets")
+    _want(a_gather, torch.int32, "a_gather")
+    if expert_offsets.numel() < table.num_experts + 1 or not expert_offsets.is_contiguous():
+        raise ValueError("expert_offsets: needs num_experts + 1 contiguous elements")
+    rows = out_rows if max_rows is None else max_rows
+    if rows > out_rows or (a_gather is not None and
+                           (a_gather.numel() < rows or not a_gather.is_contiguous())):
+        raise ValueError("max_rows exceeds the output or a_gather")
+    if a_gather is None and rows > a.shape[0]:
+        raise ValueError("without a_gather, a needs max_rows rows")
+    if a.shape[1] < table.k:
+        raise ValueError("a too narrow for the table's k")
+    return lda, _scale_matrix(a_scale, a.shape[0], _fp8_blocks(table.k), "a_scale"), rows
+
+
+def moe_w8a8_grouped_gemm(a, a_scale, table: "Fp8ExpertTable", expert_offsets, c, a_gather=None,
+                          max_rows: int | None = None, stream=None) -> None:
+    """``c[s] = (a * a_scale)[g(s)] @ W_e^T`` in BF16 for every sorted row s of every present
+    expert e of an ``Fp8ExpertTable``; see the header."""
+    c, ldc = _bf16_matrix(c, "c")
+    lda, ld_as, rows = _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows,
+                                  c.shape[0])
+    if table.gate_up:
+        raise ValueError("a gate_up table goes to moe_w8a8_grouped_gemm_swiglu")
+    if c.shape[1] < table.n:
+        raise ValueError("c too narrow for the table's n")
+    _same_device(a, a_scale, expert_offsets, c, a_gather, table.weight_ptrs)
+    _check("moe_w8a8_grouped_gemm", load().moe_w8a8_grouped_gemm(
+        _p(a), lda, _p(a_scale), ld_as, a.shape[0], _p(a_gather), _p(table.weight_ptrs),
+        _p(table.scale_ptrs), _p(expert_offsets), table.num_experts, _p(c), ldc, rows, table.n,
+        table.k, _stream(stream)))
+
+
+def moe_w8a8_grouped_gemm_swiglu(a, a_scale, table: "Fp8ExpertTable", expert_offsets, act,
+                                 act_scale, limit: float, a_gather=None,
+                                 max_rows: int | None = None, stream=None) -> None:
+    """The grouped FP8 product over a fused gate_up table (``gate_up=True``), the clamped
+    SwiGLU and the quantisation of its output: E4M3 ``act [rows, mi]`` with
+    ``act_scale [rows, ceil(mi / 128)]``."""
+    ld_act = _fp8_matrix(act, "act")
+    lda, ld_as, rows = _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows,
+                                  act.shape[0])
+    if not table.gate_up:
+        raise ValueError("the table was not made with gate_up=True")
+    mi = table.n // 2
+    if act.shape[1] < mi:
+        raise ValueError("act too narrow for the table's n / 2")
+    ld_os = _scale_matrix(act_scale, rows, _fp8_blocks(mi), "act_scale")
+    _same_device(a, a_scale, expert_offsets, act, act_scale, a_gather, table.weight_ptrs)
+    _check("moe_w8a8_grouped_gemm_swiglu", load().moe_w8a8_grouped_gemm_swiglu(
+        _p(a), lda, _p(a_scale), ld_as, a.shape[0], _p(a_gather), _p(table.weight_ptrs),
+        _p(table.scale_ptrs), _p(expert_offsets), table.num_experts, _p(act), ld_act,
+        _p(act_scale), ld_os, rows, mi, table.k, float(limit), _stream(stream)))
+
+
 # ----------------------------------------------------------------------------- helpers
 
 class SharedExpert:
@@ -876,3 +1056,151 @@ def moe_layer_decode(x, topk_ids, topk_weights, gate_up: ExpertTable, down: Expe
     if isinstance(shared, SharedExpert):
         shared = shared.for_combine(x, limit, stream)
     moe_combine(ws.expert_out[:t], ws.slot_perm[:t], topk_weights, out, shared, stream)
+
+
+# ------------------------------------------------------------------------- FP8 helpers
+
+class Fp8ExpertTable:
+    """Device pointer table of one FP8 projection for all experts.
+
+    ``weights[e]`` holds E4M3 codes ``[n, k]`` (float8_e4m3fn or uint8) and ``scales[e]``
+    float32 ``[ceil(n / 128), ceil(k / 128)]``, or both ``None`` for an expert that is not
+    present. With ``gate_up``, the weight is gate rows ``[0, n / 2)`` then up rows, and the
+    scales are the gate's blocks then the up's: ``[2 ceil(n / 2 / 128), ceil(k / 128)]``.
+    The table keeps the tensors alive.
+    """
+
+    def __init__(self, weights, scales, n: int, k: int, gate_up: bool = False, device=None):
+        import torch
+
+        if len(weights) != len(scales):
+            raise ValueError("weights and scales need one entry per expert")
+        if gate_up and n % 2:
+            raise ValueError("a gate_up table needs an even n")
+        self.n, self.k, self.num_experts = int(n), int(k), len(weights)
+        self.gate_up = bool(gate_up)
+        nb = 2 * _fp8_blocks(n // 2) if gate_up else _fp8_blocks(n)
+        s_shape = (nb, _fp8_blocks(k))
+        wp, sp = [], []
+        for e, (w, s) in enumerate(zip(weights, scales)):
+            if (w is None) != (s is None):
+                raise ValueError(f"expert {e}: weight and scales must both be present or None")
+            if w is None:
+                wp.append(0)
+                sp.append(0)
+                continue
+            if w.dtype not in (torch.float8_e4m3fn, torch.uint8) or s.dtype != torch.float32 or \
+                    not w.is_cuda or not s.is_cuda:
+                raise TypeError(f"expert {e}: expected E4M3 codes and float32 scales on a device")
+            if tuple(w.shape) != (n, k) or tuple(s.shape) != s_shape:
+                raise ValueError(f"expert {e}: expected [{n}, {k}] codes and "
+                                 f"{list(s_shape)} scales")
+            if not (w.is_contiguous() and s.is_contiguous()):
+                raise ValueError(f"expert {e}: weights and scales must be contiguous")
+            if w.data_ptr() % 16 or s.data_ptr() % 4:
+                raise ValueError(f"expert {e}: weights must be 16-byte aligned")
+            if device is None:
+                device = w.device
+            if w.device != s.device or w.device != torch.device(device):
+                raise ValueError(f"expert {e}: lies on another device")
+            wp.append(w.data_ptr())
+            sp.append(s.data_ptr())
+        if device is None:  # every entry null
+            device = torch.device("cuda", torch.cuda.current_device())
+        self._keep = (list(weights), list(scales))
+        self.weight_ptrs = torch.tensor(wp, dtype=torch.int64, device=device)
+        self.scale_ptrs = torch.tensor(sp, dtype=torch.int64, device=device)
+        self.present = [w is not None for w in weights]
+
+
+class Fp8Workspace:
+    """Every buffer one FP8 layer call needs, allocated once for up to ``max_rows``. Calls
+    that share a workspace must be ordered on one stream."""
+
+    def __init__(self, max_rows: int, top_k: int, num_experts: int, hidden: int,
+                 moe_intermediate: int, device="cuda"):
+        import torch
+
+        s = max_rows * top_k
+        i32 = dict(dtype=torch.int32, device=device)
+        f32 = dict(dtype=torch.float32, device=device)
+        f8 = dict(dtype=torch.float8_e4m3fn, device=device)
+        self.max_rows, self.top_k, self.num_experts = max_rows, top_k, num_experts
+        self.hidden, self.moe_intermediate = hidden, moe_intermediate
+        self.sorted_token_ids = torch.empty(s, **i32)
+        self.sorted_expert_ids = torch.empty(s, **i32)
+        self.expert_offsets = torch.empty(num_experts + 1, **i32)
+        self.token_to_perm = torch.empty(s, **i32)
+        self.x = torch.empty(max_rows, hidden, **f8)
+        self.x_scale = torch.empty(max_rows, _fp8_blocks(hidden), **f32)
+        self.act = torch.empty(s, moe_intermediate, **f8)
+        self.act_scale = torch.empty(s, _fp8_blocks(moe_intermediate), **f32)
+        self.expert_out = torch.empty(s, hidden, dtype=torch.bfloat16, device=device)
+
+
+class SharedExpertFp8:
+    """The shared expert in FP8: E4M3 ``gate_w``, ``up_w`` ``[I, H]`` and ``down_w`` ``[H, I]``
+    with their block scales, plus its activation and output buffers for up to ``max_rows``
+    rows. Calling it on quantised rows runs moe_dense_gate_up_swiglu_fp8 then
+    moe_dense_gemm_fp8 and returns the BF16 ``[rows, H]`` output view."""
+
+    def __init__(self, gate_w, gate_scale, up_w, up_scale, down_w, down_scale, max_rows: int):
+        import torch
+
+        inter, hidden = gate_w.shape
+        if tuple(up_w.shape) != (inter, hidden) or tuple(down_w.shape) != (hidden, inter):
+            raise ValueError("expected gate_w, up_w [I, H] and down_w [H, I]")
+        dev = gate_w.device
+        self.gate, self.up = (gate_w, gate_scale), (up_w, up_scale)
+        self.down = (down_w, down_scale)
+        self.inter, self.hidden = inter, hidden
+        self.act = torch.empty(max_rows, inter, dtype=torch.float8_e4m3fn, device=dev)
+        self.act_scale = torch.empty(max_rows, _fp8_blocks(inter), dtype=torch.float32,
+                                     device=dev)
+        self.out = torch.empty(max_rows, hidden, dtype=torch.bfloat16, device=dev)
+
+    def __call__(self, x, x_scale, limit: float, stream=None):
+        rows = x.shape[0]
+        if rows > self.act.shape[0]:
+            raise ValueError(f"{rows} rows exceed the {self.act.shape[0]} the buffers hold")
+        act, act_scale, out = self.act[:rows], self.act_scale[:rows], self.out[:rows]
+        moe_dense_gate_up_swiglu_fp8(x, x_scale, *self.gate, *self.up, act, act_scale, limit,
+                                     stream)
+        moe_dense_gemm_fp8(act, act_scale, *self.down, out, stream)
+        return out
+
+
+def moe_layer_fp8(x, topk_ids, topk_weights, gate_up: Fp8ExpertTable, down: Fp8ExpertTable,
+                  limit: float, ws: Fp8Workspace, out, shared=None, stream=None) -> None:
+    """One routed MoE layer in FP8 over the BF16 rows of ``x``, in the order of moe_layer:
+    align (and zero expert_out where experts are absent) -> quantise the rows -> grouped
+    gate_up with the SwiGLU clamp and the quantisation of its output -> grouped down ->
+    indexed combine into the BF16 ``out``. ``shared`` is the combine's shared term: a BF16
+    ``[rows, H]`` tensor, a ``SharedPartials``, a ``SharedExpertFp8`` (run over the quantised
+    rows) or a ``SharedExpert`` (run over ``x``)."""
+    _same_experts(gate_up, down)
+    rows, top_k = topk_ids.shape
+    hidden, mi = gate_up.k, gate_up.n // 2
+    if not gate_up.gate_up or down.gate_up or down.n != hidden or down.k != mi:
+        raise ValueError("expected a gate_up table [2 mi, H] and a down table [H, mi]")
+    if rows > ws.max_rows or top_k != ws.top_k or gate_up.num_experts != ws.num_experts or \
+            hidden != ws.hidden or mi != ws.moe_intermediate:
+        raise ValueError("the workspace was made for other sizes")
+    if tuple(x.shape) != (rows, hidden) or tuple(out.shape) != (rows, hidden):
+        raise ValueError(f"x and out must be [{rows}, {hidden}]")
+    s = rows * top_k
+    moe_align(topk_ids, gate_up.num_experts, ws.sorted_token_ids, ws.sorted_expert_ids,
+              ws.expert_offsets, ws.token_to_perm, None, None, stream,
+              zero=None if all(down.present) else ws.expert_out[:s])
+    xq, xs = ws.x[:rows], ws.x_scale[:rows]
+    moe_quant_fp8(x, xq, xs, stream)
+    act, act_scale = ws.act[:s], ws.act_scale[:s]
+    moe_w8a8_grouped_gemm_swiglu(xq, xs, gate_up, ws.expert_offsets, act, act_scale, limit,
+                                 ws.sorted_token_ids, stream=stream)
+    moe_w8a8_grouped_gemm(act, act_scale, down, ws.expert_offsets, ws.expert_out[:s],
+                          stream=stream)
+    if isinstance(shared, SharedExpertFp8):
+        shared = shared(xq, xs, limit, stream)
+    elif isinstance(shared, SharedExpert):
+        shared = shared.for_combine(x, limit, stream)
+    moe_combine(ws.expert_out[:s], ws.token_to_perm, topk_weights, out, shared, stream)

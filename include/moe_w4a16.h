@@ -23,6 +23,11 @@
  *                           the decode / verify path for a few rows: the union of the
  *                           rows' experts (no sort) and one sweep of each union expert,
  *                           outputs laid out by (row, slot)
+ *   moe_quant_fp8, moe_w8a8_grouped_gemm, moe_w8a8_grouped_gemm_swiglu
+ *                           the routed layer on E4M3 weights and activations with one FP32
+ *                           scale per block of 128 (W8A8)
+ *   moe_dense_gemm_fp8, moe_dense_gate_up_swiglu_fp8
+ *                           the shared expert in the same format
  *
  * Sources (the pages this library follows, by title and section):
  *   [FPG]  "Module forward_prefill_gemm" (glm5next_mlp/forward_prefill_gemm), sections
@@ -555,6 +560,132 @@ int moe_w4a16_gemv_union_swiglu(const uint16_t *a, int64_t lda, int32_t a_rows,
                                 int32_t top_k, int32_t num_experts, uint16_t *act,
                                 int64_t ld_act, int32_t mi, int32_t k, float limit,
                                 void *stream);
+
+/*
+ * The FP8 (W8A8) calls. Codes are E4M3 (OCP FN), one byte each, passed as uint8_t. A row of
+ * activations has one FP32 scale per 128 columns, a weight [n, k] one per block of 128 rows
+ * x 128 columns; the last block of a row or column may be partial. The value of a code is
+ * code * scale. With b running over the ceil(k / 128) blocks of k:
+ *
+ *   product(s, j) = sum_b a_scale[s, b] * w_scale[j / 128, b]
+ *                         * (sum_{k in block b} a[s, k] * w[j, k])
+ *
+ * The inner sums are those of the FP8 matrix cores (FP32), the outer one is FP32 in order of
+ * b (split over up to 8 waves for some sizes, joined in a fixed order): a call's results
+ * depend on its arguments alone, never on timing. NaN and infinities follow IEEE
+ * arithmetic; a row's NaN reaches only that row's outputs.
+ *
+ * Shared requirements (else MOE_EINVAL): the output width a positive multiple of 16; k a
+ * multiple of 16 in [16, MOE_FP8_MAX_K]; lda and the weight's leading dimension at least k,
+ * multiples of 16 and below 2^22; ld_a_scale >= ceil(k / 128) and below 2^20; code pointers
+ * 16-byte and scale pointers 4-byte aligned; required pointers non-NULL when there are rows.
+ * Every row count may be 0 (nothing is enqueued).
+ */
+#define MOE_FP8_MAX_K 32768
+
+/*
+ * moe_quant_fp8 - quantise BF16 rows:
+ *
+ *   scale[r, g] = max(max_{j in group g} |x[r, j]| / 448, 2^-126),   g = j / 128
+ *   q[r, j]     = e4m3_rne(x[r, j] / scale[r, g])
+ *
+ * with IEEE FP32 divisions and ties to even. No value saturates. A group of zeros gets the
+ * scale 2^-126. A NaN in a group makes its scale and codes NaN (code 0x7F or 0xFF); an
+ * infinity makes the scale infinite, its own code NaN and finite values' codes 0.
+ *
+ *   x      bf16  [rows, ld_x]
+ *   q      e4m3  [rows, ld_q]      out
+ *   scale  float [rows, ld_scale]  out: ceil(cols / 128) per row
+ * Requirements (else MOE_EINVAL): rows >= 0; cols >= 0 and cols % 16 == 0; ld_x >= cols, a
+ * multiple of 8; ld_q >= cols, a multiple of 16; ld_scale >= ceil(cols / 128); x and q
+ * 16-byte aligned, scale 4-byte aligned, non-NULL when rows * cols > 0; fewer than 2^28
+ * groups.
+ */
+int moe_quant_fp8(const uint16_t *x, int64_t ld_x, uint8_t *q, int64_t ld_q, float *scale,
+                  int64_t ld_scale, int32_t rows, int32_t cols, void *stream);
+
+/*
+ * moe_dense_gemm_fp8 - c[i, j] = bf16( product(i, j) ) for i < m, j < n: the shared expert's
+ * down projection with FP8 operands.
+ *
+ *   a        e4m3  [m, lda],  a_scale float [m, ld_a_scale]
+ *   b        e4m3  [n, ldb],  b_scale float [ceil(n / 128), ceil(k / 128)] contiguous
+ *   c        bf16  [m, ldc]   output; ldc >= n and a multiple of 8, c 16-byte aligned
+ */
+int moe_dense_gemm_fp8(const uint8_t *a, int64_t lda, const float *a_scale, int64_t ld_a_scale,
+                       const uint8_t *b, int64_t ldb, const float *b_scale, uint16_t *c,
+                       int64_t ldc, int32_t m, int32_t n, int32_t k, void *stream);
+
+/*
+ * moe_dense_gate_up_swiglu_fp8 - the shared expert's gate and up projections, its SwiGLU and
+ * the quantisation of its output in one launch:
+ *
+ *   v[i, j] = silu(min(G, limit)) * clamp(U, -limit, limit)
+ *   G = product with gate_w, U = product with up_w   (FP32, not rounded in between)
+ *   act, act_scale = v quantised as moe_quant_fp8 quantises (its input here is FP32)
+ *
+ *   gate_w, up_w          e4m3 [inter, ldw] each
+ *   gate_scale, up_scale  float [ceil(inter / 128), ceil(k / 128)] contiguous
+ *   act                   e4m3 [m, ld_act] out; ld_act >= inter and a multiple of 16
+ *   act_scale             float [m, ld_act_scale] out; ld_act_scale >= ceil(inter / 128)
+ * Also required: limit > 0.
+ */
+int moe_dense_gate_up_swiglu_fp8(const uint8_t *a, int64_t lda, const float *a_scale,
+                                 int64_t ld_a_scale, const uint8_t *gate_w,
+                                 const float *gate_scale, const uint8_t *up_w,
+                                 const float *up_scale, int64_t ldw, uint8_t *act,
+                                 int64_t ld_act, float *act_scale, int64_t ld_act_scale,
+                                 int32_t m, int32_t inter, int32_t k, float limit, void *stream);
+
+/*
+ * moe_w8a8_grouped_gemm - moe_w4a16_grouped_gemm with FP8 operands: for every expert e whose
+ * weight_ptrs[e] is non-zero and every sorted row s in [expert_offsets[e],
+ * expert_offsets[e + 1]) (clipped to [0, max_rows)):
+ *
+ *   c[s, j] = bf16( product(g(s), j) ) with expert e's weight,  g(s) = a_gather ? a_gather[s] : s
+ *
+ *   a, a_scale      e4m3 [a_rows, lda], float [a_rows, ld_a_scale]
+ *   a_gather        int32 [max_rows] or NULL. An index outside [0, a_rows) reads zeros.
+ *   weight_ptrs     uint64 [num_experts] device addresses of e4m3 [n, k], contiguous and
+ *                   16-byte aligned (0 = expert not present: its rows of c are not written)
+ *   scale_ptrs      uint64 [num_experts] device addresses of float [ceil(n / 128),
+ *                   ceil(k / 128)] (non-zero where weight_ptrs is)
+ *   expert_offsets  int32 [num_experts + 1] as written by moe_align (a prefix sum; other
+ *                   values are not checked: rows may then be missed, but each row the call
+ *                   reads or writes still lies in [0, max_rows))
+ *   c               bf16 [max_rows, ldc]; ldc >= n and a multiple of 8, 16-byte aligned. Rows
+ *                   no present expert covers are not written.
+ * Experts without rows cost nothing, so there is no active-expert list to pass.
+ * Also required: 1 <= num_experts <= MOE_ALIGN_MAX_EXPERTS; without a gather, a_rows >=
+ * max_rows; with one, a_rows * lda and a_rows * ld_a_scale * 4 below 2^31.
+ */
+int moe_w8a8_grouped_gemm(const uint8_t *a, int64_t lda, const float *a_scale,
+                          int64_t ld_a_scale, int32_t a_rows, const int32_t *a_gather,
+                          const uint64_t *weight_ptrs, const uint64_t *scale_ptrs,
+                          const int32_t *expert_offsets, int32_t num_experts, uint16_t *c,
+                          int64_t ldc, int32_t max_rows, int32_t n, int32_t k, void *stream);
+
+/*
+ * moe_w8a8_grouped_gemm_swiglu - the grouped product over a fused gate_up weight (2 mi rows:
+ * gate rows [0, mi), up rows [mi, 2 mi)) with the SwiGLU clamp and the quantisation of its
+ * output, as in moe_dense_gate_up_swiglu_fp8, per expert:
+ *
+ *   act[s, 0..mi), act_scale[s, 0..ceil(mi / 128))
+ *
+ *   weight_ptrs  addresses of e4m3 [2 mi, k], contiguous
+ *   scale_ptrs   addresses of float [2 ceil(mi / 128), ceil(k / 128)]: the gate's blocks, then
+ *                the up's (two separately quantised projections one after the other; their
+ *                blocks start at each projection's first row also where mi % 128 != 0)
+ * The other arguments and requirements as moe_w8a8_grouped_gemm and
+ * moe_dense_gate_up_swiglu_fp8. Rows no present expert covers are not written.
+ */
+int moe_w8a8_grouped_gemm_swiglu(const uint8_t *a, int64_t lda, const float *a_scale,
+                                 int64_t ld_a_scale, int32_t a_rows, const int32_t *a_gather,
+                                 const uint64_t *weight_ptrs, const uint64_t *scale_ptrs,
+                                 const int32_t *expert_offsets, int32_t num_experts,
+                                 uint8_t *act, int64_t ld_act, float *act_scale,
+                                 int64_t ld_act_scale, int32_t max_rows, int32_t mi, int32_t k,
+                                 float limit, void *stream);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,7 @@ imports, calls or links anything here, and this package shares no code with it.
 
 Modules:
 - ``codecs``: E2M1 / E4M3FN decode, FP32 -> BF16 round-to-nearest-even.
+- ``fp8``: E4M3 rounding, block scales, the block-scaled products and the FP8 routed layer.
 - ``moe``: dequant (exact and BF16-weight modes), align, grouped GEMM, SwiGLU clamp,
   combine, the whole routed layer, the router top-k, and the shared expert (a BF16
   SwiGLU MLP).
@@ -23,4 +24,4 @@ numbers cannot be reproduced; only the structural fact that the grouped GEMM's e
 against a BF16-weight reference is about half an output BF16 ulp is checked.
 """
 
-from . import codecs, moe  # noqa: F401
+from . import codecs, fp8, moe  # noqa: F401
