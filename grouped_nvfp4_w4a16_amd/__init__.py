@@ -45,7 +45,7 @@ __all__ = [
     "moe_dense_gemm_bf16_partials", "moe_combine_partials", "SharedPartials",
     "moe_quant_fp8", "moe_dense_gemm_fp8", "moe_dense_gate_up_swiglu_fp8",
     "moe_w8a8_grouped_gemm", "moe_w8a8_grouped_gemm_swiglu", "Fp8ExpertTable", "Fp8Workspace",
-    "SharedExpertFp8", "moe_layer_fp8", "FP8_MAX_K",
+    "SharedExpertFp8", "moe_layer_fp8", "FP8_MAX_K", "moe_fp8_swiglu_workspace_bytes",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_w4a16.so")
@@ -61,6 +61,7 @@ EXPORTS = (
     "moe_align_zero", "moe_dense_splitk_ways", "moe_dense_gemm_bf16_partials",
     "moe_combine_partials", "moe_quant_fp8", "moe_dense_gemm_fp8",
     "moe_dense_gate_up_swiglu_fp8", "moe_w8a8_grouped_gemm", "moe_w8a8_grouped_gemm_swiglu",
+    "moe_fp8_swiglu_workspace_bytes",
 )
 
 UNION_MAX_IDS = 1024  # MOE_UNION_MAX_IDS: rows * top_k of moe_row_union
@@ -123,13 +124,14 @@ _SIGNATURES = {
                             _vp], ctypes.c_int),
     "moe_dense_gate_up_swiglu_fp8": (
         [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _i32,
-         _f32, _vp], ctypes.c_int),
+         _f32, _vp, _i64, _vp], ctypes.c_int),
+    "moe_fp8_swiglu_workspace_bytes": ([_i32, _i32, _i32, _i32], _i64),
     "moe_w8a8_grouped_gemm": (
         [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp],
         ctypes.c_int),
     "moe_w8a8_grouped_gemm_swiglu": (
         [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _i64, _i32, _i32,
-         _i32, _f32, _vp], ctypes.c_int),
+         _i32, _f32, _vp, _i64, _vp], ctypes.c_int),
 }
 
 
@@ -184,14 +186,15 @@ def _check(name: str, status: int) -> None:
 
 
 def _p(t):
-    return None if t is None else _vp(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     import torch
 
-    s = torch.cuda.current_stream() if stream is None else stream
-    return _vp(s.cuda_stream)
+    if stream is None:  # the current stream's handle, without making a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _want(t, dtype, name):
@@ -720,11 +723,39 @@ def moe_dense_gemm_fp8(a, a_scale, b, b_scale, c, stream=None) -> None:
         _stream(stream)))
 
 
+def moe_fp8_swiglu_workspace_bytes(rows: int, num_experts: int, width: int, k: int) -> int:
+    """Bytes of the workspace moe_w8a8_grouped_gemm_swiglu (``width`` = mi) or, with
+    ``num_experts`` 0, moe_dense_gate_up_swiglu_fp8 (``width`` = inter) splits these sizes
+    with; 0 where they are not split."""
+    return int(load().moe_fp8_swiglu_workspace_bytes(int(rows), int(num_experts), int(width),
+                                                     int(k)))
+
+
+def _swiglu_workspace(ws, rows, num_experts, width, k, device, stream):
+    """(tensor or None, pointer, bytes) of a SwiGLU call's workspace: the caller's, or one from
+    torch's caching allocator for this call (reused only behind it on its stream)."""
+    import torch
+
+    if ws is not None:
+        wp, wb = _workspace(ws)
+        _same_device(ws)
+        return ws, wp, wb
+    need = load().moe_fp8_swiglu_workspace_bytes(rows, num_experts, width, k)
+    if need == 0:
+        return None, None, 0
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws, _p(ws), need
+
+
 def moe_dense_gate_up_swiglu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale, act, act_scale,
-                                 limit: float, stream=None) -> None:
+                                 limit: float, stream=None, workspace=None) -> None:
     """The shared expert's gate and up products (``gate_w``, ``up_w`` E4M3 ``[I, K]``, same
-    strides), the clamped SwiGLU and the quantisation of its output in one launch: E4M3
-    ``act [M, I]`` with ``act_scale [M, ceil(I / 128)]``."""
+    strides), the clamped SwiGLU and the quantisation of its output: E4M3 ``act [M, I]`` with
+    ``act_scale [M, ceil(I / 128)]``. Sizes with few tiles run split over K through
+    ``workspace``, a uint8 device tensor of moe_fp8_swiglu_workspace_bytes(M, 0, I, K) bytes;
+    without one, the call takes it from torch's caching allocator."""
     lda, ldw = _fp8_matrix(a, "a"), _fp8_matrix(gate_w, "gate_w")
     ld_act = _fp8_matrix(act, "act")
     if _fp8_matrix(up_w, "up_w") != ldw or up_w.shape != gate_w.shape:
@@ -740,9 +771,11 @@ def moe_dense_gate_up_swiglu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale,
     _scale_matrix(up_scale, ib, kb, "up_scale", contiguous=True)
     ld_os = _scale_matrix(act_scale, m, ib, "act_scale")
     _same_device(a, a_scale, gate_w, gate_scale, up_w, up_scale, act, act_scale)
+    ws, wp, wb = _swiglu_workspace(workspace, m, 0, inter, k, a.device, stream)
     _check("moe_dense_gate_up_swiglu_fp8", load().moe_dense_gate_up_swiglu_fp8(
         _p(a), lda, _p(a_scale), ld_as, _p(gate_w), _p(gate_scale), _p(up_w), _p(up_scale), ldw,
-        _p(act), ld_act, _p(act_scale), ld_os, m, inter, k, float(limit), _stream(stream)))
+        _p(act), ld_act, _p(act_scale), ld_os, m, inter, k, float(limit), wp, wb,
+        _stream(stream)))
 
 
 def _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows, out_rows):
@@ -785,10 +818,12 @@ def moe_w8a8_grouped_gemm(a, a_scale, table: "Fp8ExpertTable", expert_offsets, c
 
 def moe_w8a8_grouped_gemm_swiglu(a, a_scale, table: "Fp8ExpertTable", expert_offsets, act,
                                  act_scale, limit: float, a_gather=None,
-                                 max_rows: int | None = None, stream=None) -> None:
+                                 max_rows: int | None = None, stream=None,
+                                 workspace=None) -> None:
     """The grouped FP8 product over a fused gate_up table (``gate_up=True``), the clamped
     SwiGLU and the quantisation of its output: E4M3 ``act [rows, mi]`` with
-    ``act_scale [rows, ceil(mi / 128)]``."""
+    ``act_scale [rows, ceil(mi / 128)]``. ``workspace`` as for moe_dense_gate_up_swiglu_fp8
+    (moe_fp8_swiglu_workspace_bytes(rows, num_experts, mi, k) bytes)."""
     ld_act = _fp8_matrix(act, "act")
     lda, ld_as, rows = _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows,
                                   act.shape[0])
@@ -799,10 +834,12 @@ def moe_w8a8_grouped_gemm_swiglu(a, a_scale, table: "Fp8ExpertTable", expert_off
         raise ValueError("act too narrow for the table's n / 2")
     ld_os = _scale_matrix(act_scale, rows, _fp8_blocks(mi), "act_scale")
     _same_device(a, a_scale, expert_offsets, act, act_scale, a_gather, table.weight_ptrs)
+    ws, wp, wb = _swiglu_workspace(workspace, rows, table.num_experts, mi, table.k, a.device,
+                                   stream)
     _check("moe_w8a8_grouped_gemm_swiglu", load().moe_w8a8_grouped_gemm_swiglu(
         _p(a), lda, _p(a_scale), ld_as, a.shape[0], _p(a_gather), _p(table.weight_ptrs),
         _p(table.scale_ptrs), _p(expert_offsets), table.num_experts, _p(act), ld_act,
-        _p(act_scale), ld_os, rows, mi, table.k, float(limit), _stream(stream)))
+        _p(act_scale), ld_os, rows, mi, table.k, float(limit), wp, wb, _stream(stream)))
 
 
 # ----------------------------------------------------------------------------- helpers

@@ -46,11 +46,14 @@ using moe::u32x4_t;
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 
+constexpr int kLgkmWaitImm = 0xC07F;  // s_waitcnt lgkmcnt(0), no vmcnt or expcnt wait
 constexpr int kRowBytes = kFp8Block;  // one LDS row: 128 k
 constexpr int kMaxK = MOE_FP8_MAX_K;  // the weight scales of a tile's K sit in LDS
+constexpr int kGroupM = 4;              // row tiles that run next to each other
 constexpr int kMaxExperts = MOE_ALIGN_MAX_EXPERTS;
 
 struct GemmArgs {
@@ -74,12 +77,19 @@ struct GemmArgs {
   int32_t n;                // output columns
   int32_t k;
   float limit;
+  float *partial;           // split-K SwiGLU: FP32 sums [ways][rows][2][n] instead of q
+  int32_t ways;             // splits of K (1: none)
 };
 
 // Compile-time shape of a kernel: NT 16-row weight tiles and TT 16-row row tiles per wave,
-// WN x WT waves over the tile, KS slice groups, ST stages.
-template <int NT_, int TT_, int WN_, int WT_, int KS_, int ST_>
+// WN x WT waves over the tile, KS slice groups, ST stages. kWide: 32 x 32 products in the
+// two-phase loop.
+template <int NT_, int TT_, int WN_, int WT_, int KS_, int ST_, bool kWide_ = false>
 struct Cfg {
+  static constexpr bool kWide = kWide_;
+  static constexpr int kTileRows = kWide ? 32 : 16;  // rows of a row tile
+  static_assert(!kWide || (NT_ == 4 && TT_ == 4 && WN_ * WT_ == 8 && KS_ == 1 && ST_ >= 3),
+                "the two-phase loop: 64 x 64 per wave");
   static constexpr int NT = NT_, TT = TT_, WN = WN_, WT = WT_, KS = KS_, ST = ST_;
   static constexpr int BN = 16 * NT * WN, BT = 16 * TT * WT;
   static constexpr int kSliceWaves = WN * WT;
@@ -93,11 +103,12 @@ struct Cfg {
   static constexpr int kXInstr = BT / 8;
   static constexpr int kXLoads = kXInstr > kSliceWaves ? kXInstr / kSliceWaves : 1;
   static constexpr int kLoads = kWLoads + kXLoads + 1;
-  static constexpr int kNBlocks = BN > kFp8Block ? BN / kFp8Block : 1;  // weight scale rows
+  static constexpr int kNBlocks = BN > kFp8Block ? 2 : 1;  // weight scale rows
+  static_assert(BN <= 2 * kFp8Block, "at most two scale blocks");
   static_assert(BN / 8 % kSliceWaves == 0, "whole weight instructions per wave");
   static_assert(kXInstr % kSliceWaves == 0 || kXInstr < kSliceWaves, "row instructions");
   static_assert(kSliceWaves * 64 >= BT, "one scale instruction per wave covers the tile");
-  static_assert(BN % kFp8Block == 0 || kFp8Block % BN == 0, "scale blocks");
+  static_assert(BN % 64 == 0 || kFp8Block % BN == 0, "a tile's rows lie in kNBlocks blocks");
   // LDS: stages, a dump for loads that must not land anywhere, weight scales, tile prefix
   static constexpr int kDumpOff = ST * kStage;
   static constexpr int kSbOff = kDumpOff + 1024;
@@ -159,44 +170,74 @@ struct Bf16Mma {
   }
 };
 
-template <class C, bool kGrouped>
-int lds_bytes(const GemmArgs &p) {
-  const int kb = (p.k + kFp8Block - 1) / kFp8Block;
-  const int kb_pad = (kb + C::KS - 1) / C::KS * C::KS;
-  return C::kSbOff + 4 * C::kNBlocks * kb_pad + (kGrouped ? 4 * (p.num_experts + 1) : 0);
-}
+// The same for 32 x 32 x 128 block products (half the matrix instructions per output). A lane
+// holds 64 codes of a row, two lanes per row.
+struct WideCodes {
+  u32x4_t piece[4];
+};
 
-template <class C, bool kSwiglu, bool kGrouped>
-__global__ __launch_bounds__(C::kThreads) void fp8_gemm_kernel(const GemmArgs p) {
-  static_assert(!kSwiglu || (C::BN == 2 * kFp8Block && C::KS == 1 && C::NT % 2 == 0),
-                "the SwiGLU form owns whole output groups");
-  constexpr int NT = C::NT, TT = C::TT, WN = C::WN, KS = C::KS, ST = C::ST;
-  constexpr int BN = C::BN, BT = C::BT;
-  constexpr int kBnOut = kSwiglu ? BN / 2 : BN;  // output columns per tile
-  using Mma = std::conditional_t<kSwiglu, Bf16Mma, Fp8Mma>;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+struct Fp8Wide {
+  struct Operand {
+    i32x8_t part[2];
+  };
+  static constexpr int kParts = 2;
+  static __device__ __forceinline__ Operand operand(const WideCodes &c) {
+    Operand o;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      o.part[j] = __builtin_bit_cast(
+          i32x8_t, __builtin_shufflevector(c.piece[2 * j], c.piece[2 * j + 1], 0, 1, 2, 3, 4, 5,
+                                           6, 7));
+    return o;
+  }
+  static __device__ __forceinline__ f32x16_t mma(const i32x8_t &w, const i32x8_t &x, f32x16_t d) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, d, 0, 0, 0, 0, 0, 0);
+  }
+};
 
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int slice = wave / C::kSliceWaves, sw = wave % C::kSliceWaves;
-  const int wn = sw % WN, wt = sw / WN;
-  const int r16 = lane & 15, g4 = lane >> 4;
+struct Bf16Wide {
+  struct Operand {
+    bf16x8_t part[8];
+  };
+  static constexpr int kParts = 8;
+  static __device__ __forceinline__ Operand operand(const WideCodes &c) {
+    Operand o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o.part[2 * j] = Bf16Mma::eight(c.piece[j][0], c.piece[j][1]);
+      o.part[2 * j + 1] = Bf16Mma::eight(c.piece[j][2], c.piece[j][3]);
+    }
+    return o;
+  }
+  static __device__ __forceinline__ f32x16_t mma(const bf16x8_t &w, const bf16x8_t &x,
+                                                 f32x16_t d) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, x, d, 0, 0, 0);
+  }
+};
 
-  const int kb_n = (p.k + kFp8Block - 1) / kFp8Block;
-  const int steps = (kb_n + KS - 1) / KS;
-  float *sb = reinterpret_cast<float *>(lds + C::kSbOff);  // [kNBlocks][steps * KS]
-  int *prefix = reinterpret_cast<int *>(sb + C::kNBlocks * steps * KS);
-  const int n_tiles = (p.n + kBnOut - 1) / kBnOut;
+// One unit of work: rows [m0, m0 + cnt) of expert (or matrix) w0 / w1 and output columns
+// [n0, n0 + n_valid).
+struct Item {
+  const uint8_t *w0, *w1;
+  const float *s0, *s1;
+  int m0, cnt, n0, n_valid;
+};
 
-  int64_t items;
-  if constexpr (kGrouped) {
-    // Row tiles per expert (none where it is absent), summed over the experts: wave 0.
+// The items of a launch with tiles of BT rows x kBnOut output columns. Grouped: `prefix`
+// (LDS, num_experts + 1) holds the row tiles before each expert, counted from the offsets.
+template <int BT, int kBnOut, bool kGrouped>
+struct Items {
+  // Every thread of the block calls it (it holds a barrier).
+  static __device__ __forceinline__ int64_t count(const GemmArgs &p, int *prefix, int lane,
+                                                  int wave) {
+    const int n_tiles = (p.n + kBnOut - 1) / kBnOut;
+    if constexpr (!kGrouped) return static_cast<int64_t>((p.rows + BT - 1) / BT) * n_tiles;
     if (wave == 0) {
       int carry = 0;
       for (int base = 0; base < p.num_experts; base += 64) {
         const int e = base + lane;
         int t = 0;
-        if (e < p.num_experts && p.w_ptrs[e] != 0) {
+        if (e < p.num_experts && p.w_ptrs[e] != 0) {  // none where the expert is absent
           const int cnt = min(p.offsets[e + 1], p.rows) - max(p.offsets[e], 0);
           t = cnt > 0 ? (cnt + BT - 1) / BT : 0;
         }
@@ -212,19 +253,18 @@ __global__ __launch_bounds__(C::kThreads) void fp8_gemm_kernel(const GemmArgs p)
       if (lane == 0) prefix[p.num_experts] = carry;
     }
     __syncthreads();
-    items = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(prefix[p.num_experts])) * n_tiles;
-  } else {
-    items = static_cast<int64_t>((p.rows + BT - 1) / BT) * n_tiles;
+    return static_cast<int64_t>(__builtin_amdgcn_readfirstlane(prefix[p.num_experts])) * n_tiles;
   }
 
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    // ---- the item: rows [m0, m0 + cnt) and output columns [n0, n0 + n_valid)
-    const int ty = static_cast<int>(item / n_tiles);
-    const int n0 = static_cast<int>(item - static_cast<int64_t>(ty) * n_tiles) * kBnOut;
-    const uint8_t *w0, *w1;
-    const float *s0, *s1;
-    int m0, cnt;
+  // Item number `item`; false for a number that offsets which are no prefix sum lead out of
+  // the expert's rows (every access so stays in range).
+  static __device__ __forceinline__ bool get(const GemmArgs &p, const int *prefix, int lane,
+                                             int64_t item, Item &it) {
+    const int n_tiles = (p.n + kBnOut - 1) / kBnOut;
+    int lo, hi;     // the expert's rows
+    int64_t local;  // the item's number within the expert
     if constexpr (kGrouped) {
+      const int ty = static_cast<int>(item / n_tiles);
       // The last expert whose prefix is at most ty (prefixes do not decrease).
       int below = 0;
       for (int base = 0; base < p.num_experts; base += 64) {
@@ -232,46 +272,213 @@ __global__ __launch_bounds__(C::kThreads) void fp8_gemm_kernel(const GemmArgs p)
         below += __popcll(__ballot(e < p.num_experts && prefix[e] <= ty));
       }
       const int e = max(below - 1, 0);
-      const int lo = max(p.offsets[e], 0), hi = min(p.offsets[e + 1], p.rows);
-      const int tile = ty - __builtin_amdgcn_readfirstlane(prefix[e]);
-      const int64_t first = lo + static_cast<int64_t>(tile) * BT;
-      // Never true for offsets that are a prefix sum; keeps every access in range if not.
-      if (first < lo || first >= hi) continue;
-      m0 = static_cast<int>(first);
-      cnt = min(BT, hi - m0);
-      w0 = reinterpret_cast<const uint8_t *>(p.w_ptrs[e]);
-      s0 = reinterpret_cast<const float *>(p.s_ptrs[e]);
-      if (w0 == nullptr) continue;
-      w1 = w0 + static_cast<int64_t>(p.n) * p.ldw;
-      s1 = s0 + static_cast<int64_t>((p.n + kFp8Block - 1) / kFp8Block) * kb_n;
+      lo = max(p.offsets[e], 0);
+      hi = min(p.offsets[e + 1], p.rows);
+      local = item - static_cast<int64_t>(__builtin_amdgcn_readfirstlane(prefix[e])) * n_tiles;
+      it.w0 = reinterpret_cast<const uint8_t *>(p.w_ptrs[e]);
+      it.s0 = reinterpret_cast<const float *>(p.s_ptrs[e]);
+      if (it.w0 == nullptr || hi <= lo || local < 0) return false;
+      it.w1 = it.w0 + static_cast<int64_t>(p.n) * p.ldw;
+      it.s1 = it.s0 + static_cast<int64_t>((p.n + kFp8Block - 1) / kFp8Block) *
+                          ((p.k + kFp8Block - 1) / kFp8Block);
     } else {
-      m0 = ty * BT;
-      cnt = min(BT, p.rows - m0);
-      w0 = p.w0;
-      w1 = p.w1;
-      s0 = p.ws0;
-      s1 = p.ws1;
+      lo = 0;
+      hi = p.rows;
+      local = item;
+      it.w0 = p.w0;
+      it.w1 = p.w1;
+      it.s0 = p.ws0;
+      it.s1 = p.ws1;
     }
-    const int n_valid = min(kBnOut, p.n - n0);
+    // Within an expert, kGroupM row tiles at a time, the row tile fastest: the items that run
+    // at once share both weight tiles and row tiles.
+    const int m_tiles = (hi - lo + BT - 1) / BT;
+    const int64_t grp = local / (static_cast<int64_t>(kGroupM) * n_tiles);
+    const int g0 = static_cast<int>(grp) * kGroupM;
+    if (g0 >= m_tiles) return false;
+    const int g_rows = min(kGroupM, m_tiles - g0);
+    const int in_grp = static_cast<int>(local - grp * kGroupM * n_tiles);
+    it.n0 = in_grp / g_rows * kBnOut;
+    // The tiles of an expert hold equal numbers of rows (a multiple of 16): as many as BT allows
+    // at least, none with a few leftover rows that would cost it all the expert's weights.
+    const int per = kGrouped ? ((hi - lo + m_tiles - 1) / m_tiles + 15) / 16 * 16 : BT;
+    it.m0 = lo + (g0 + in_grp % g_rows) * per;
+    it.cnt = min(per, hi - it.m0);
+    it.n_valid = min(kBnOut, p.n - it.n0);
+    return it.n0 < p.n && it.cnt > 0;
+  }
+};
+
+// This block's share of the items: workgroups go to the 8 XCDs round-robin, and each XCD
+// takes a contiguous eighth, so that items with the same rows or weights run next to each
+// other on one L2.
+struct Share {
+  int64_t first, end;
+  int stride;
+};
+
+__device__ __forceinline__ Share share_of(int64_t items) {
+  const int stride = gridDim.x;
+  if ((stride & 7) != 0) return {static_cast<int64_t>(blockIdx.x), items, stride};
+  const int xcd = blockIdx.x & 7;
+  return {items * xcd / 8 + (blockIdx.x >> 3), items * (xcd + 1) / 8, stride >> 3};
+}
+
+// The item's rows as buffer resources: from the tile's first row, or (gathered) from row 0.
+struct Rows {
+  __amdgpu_buffer_rsrc_t codes, scales;
+  const int32_t *gather;  // of the tile's first row, or NULL
+  int cnt, a_rows;
+
+  __device__ __forceinline__ Rows(const GemmArgs &p, const Item &it)
+      : gather(p.gather != nullptr ? p.gather + it.m0 : nullptr), cnt(it.cnt), a_rows(p.a_rows) {
+    const int64_t base = gather != nullptr ? 0 : it.m0;
+    const int64_t rows = gather != nullptr ? p.a_rows : it.cnt;
+    codes = make_rsrc(p.a + base * p.lda, static_cast<uint32_t>(rows * p.lda));
+    scales = make_rsrc(p.a_scale + base * p.ld_as, static_cast<uint32_t>(rows * p.ld_as * 4));
+  }
+
+  // Row of the resources that tile row r reads, -1 for zeros.
+  __device__ __forceinline__ int source(int r) const {
+    if (r >= cnt) return -1;
+    if (gather == nullptr) return r;
+    const int t = gather[r];
+    return t >= 0 && t < a_rows ? t : -1;
+  }
+};
+
+// The tile's weight scales for all of K, sb[blk][kb_pad] in LDS, zeros past K and past the
+// last block row; blk: the gate's and the up's block (SwiGLU), or consecutive blocks. The
+// loads are issued with the item's other small loads, before the stages', and stored after
+// the stages' are on their way, so that no wait for them drains the stages.
+template <int kNBlocks, int kThreads, bool kSwiglu>
+struct WeightScales {
+  static constexpr int kPer = (kNBlocks * (kMaxK / kFp8Block + 8) + kThreads - 1) / kThreads;
+  float v[kPer];
+
+  __device__ __forceinline__ void load(const GemmArgs &p, const Item &it, int kb_pad, int tid) {
+    const int kb_n = (p.k + kFp8Block - 1) / kFp8Block, nb = (p.n + kFp8Block - 1) / kFp8Block;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int i = tid + u * kThreads;
+      const int blk = kNBlocks > 1 && i >= kb_pad ? 1 : 0, kb = i - blk * kb_pad;
+      const int row = it.n0 / kFp8Block + (kSwiglu ? 0 : blk);
+      v[u] = 0.0f;
+      if (kb < kb_n && row < nb)
+        v[u] = (kSwiglu && blk != 0 ? it.s1 : it.s0)[static_cast<int64_t>(row) * kb_n + kb];
+    }
+  }
+
+  __device__ __forceinline__ void store(float *sb, int kb_pad, int tid) const {
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      if (tid + u * kThreads < kNBlocks * kb_pad) sb[tid + u * kThreads] = v[u];
+  }
+};
+
+// The SwiGLU form's epilogue. acc[i][t][x] is gate column col(i) + 4 gl + x of tile row
+// kR row(t) + rl (rl = lane % kR, gl = lane / kR), acc[i + NT / 2][t][x] the same column's up
+// sum; WN waves hold the 128 columns of a row. `lds` is free for BT rows of codes and (WN + 1) BT floats.
+constexpr int kCodeRow = kFp8Block + 16;  // staged code row, padded
+constexpr int swiglu_epilogue_bytes(int bt, int wn) { return bt * kCodeRow + 4 * wn * bt; }
+
+template <int NT, int TT, int kR, int WN, int BT, int kThreads, class Col, class Row>
+__device__ __forceinline__ void swiglu_epilogue(const GemmArgs &p, const Item &it, uint8_t *lds,
+                                                f32x4_t (&acc)[NT][TT], Col col, Row row,
+                                                int wn, int tid) {
+  constexpr int kH = NT / 2;
+  const int lane = tid & 63, rl = lane % kR, gl = lane / kR;
+  uint32_t *red = reinterpret_cast<uint32_t *>(lds + BT * kCodeRow);  // [WN][BT] magnitudes
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < kH; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float v = moe::swiglu_clamp1(acc[i][t][x], acc[i + kH][t][x], p.limit);
+        acc[i][t][x] = v;
+        // the width is a multiple of 16: a tile of 8 or 16 columns lies inside it or past it
+        if (col(i) < it.n_valid) m = max(m, __float_as_uint(v) & 0x7FFFFFFFu);
+      }
+#pragma unroll
+    for (int d = kR; d < 64; d <<= 1)
+      m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, 64)));
+    if (gl == 0) red[wn * BT + kR * row(t) + rl] = m;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int r = kR * row(t) + rl;
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < WN; ++w) m = max(m, red[w * BT + r]);
+    const float s = moe::fp8_scale(m);
+    if (wn == 0 && gl == 0 && r < it.cnt)
+      p.q_scale[static_cast<int64_t>(it.m0 + r) * p.ld_qs + it.n0 / kFp8Block] = s;
+#pragma unroll
+    for (int i = 0; i < kH; ++i)
+      *reinterpret_cast<uint32_t *>(lds + r * kCodeRow + col(i) + 4 * gl) =
+          moe::e4m3x4(acc[i][t][0] / s, acc[i][t][1] / s, acc[i][t][2] / s, acc[i][t][3] / s);
+  }
+  __syncthreads();
+  for (int u = tid; u < BT * (kFp8Block / 16); u += kThreads) {
+    const int r = u / (kFp8Block / 16), ch = u % (kFp8Block / 16);
+    if (r >= it.cnt || ch * 16 >= it.n_valid) continue;
+    *reinterpret_cast<u32x4_t *>(p.q + static_cast<int64_t>(it.m0 + r) * p.ldc + it.n0 +
+                                 ch * 16) =
+        *reinterpret_cast<const u32x4_t *>(lds + r * kCodeRow + ch * 16);
+  }
+}
+
+template <class C, bool kGrouped>
+int lds_bytes(const GemmArgs &p) {
+  const int kb = (p.k + kFp8Block - 1) / kFp8Block;
+  const int kb_pad = (kb + C::KS - 1) / C::KS * C::KS;
+  return C::kSbOff + 4 * C::kNBlocks * kb_pad + (kGrouped ? 4 * (p.num_experts + 1) : 0);
+}
+
+template <class C, bool kSwiglu, bool kGrouped>
+__global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))) void
+fp8_gemm_kernel(GemmArgs p) {
+  static_assert(!kSwiglu || (C::BN == 2 * kFp8Block && C::KS == 1 && C::NT % 2 == 0),
+                "the SwiGLU form owns whole output groups");
+  constexpr int NT = C::NT, TT = C::TT, WN = C::WN, WT = C::WT, KS = C::KS, ST = C::ST;
+  constexpr int BN = C::BN, BT = C::BT;
+  constexpr bool kWide = C::kWide;
+  constexpr int kBnOut = kSwiglu ? BN / 2 : BN;  // output columns per tile
+  using Mma = std::conditional_t<kSwiglu, Bf16Mma, Fp8Mma>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int slice = wave / C::kSliceWaves, sw = wave % C::kSliceWaves;
+  const int wn = sw % WN, wt = sw / WN;
+  const int r16 = lane & 15, g4 = lane >> 4;
+
+  const int kb_n = (p.k + kFp8Block - 1) / kFp8Block;
+  const int kb_pad = (kb_n + KS - 1) / KS * KS;
+  float *sb = reinterpret_cast<float *>(lds + C::kSbOff);  // [kNBlocks][kb_pad]
+  int *prefix = reinterpret_cast<int *>(sb + C::kNBlocks * kb_pad);
+  using Work = Items<BT, kBnOut, kGrouped>;
+  const int64_t tiles = Work::count(p, prefix, lane, wave);
+  const int ways = kSwiglu ? p.ways : 1;
+  const int split_kb = (kb_n + ways - 1) / ways;  // K blocks per split
+  const Share mine = share_of(tiles * ways);
+
+  for (int64_t item = mine.first; item < mine.end; item += mine.stride) {
+    Item it;
+    const int split = ways > 1 ? static_cast<int>(item / tiles) : 0;
+    if (!Work::get(p, prefix, lane, item - split * tiles, it)) continue;
+    const int kb0 = split * split_kb, kb1 = min(kb_n, kb0 + split_kb);  // this item's K blocks
+    const int steps = max(kb1 - kb0 + KS - 1, 0) / KS;
+    const int n0 = it.n0, n_valid = it.n_valid, m0 = it.m0, cnt = it.cnt;
     const uint32_t w_bytes = static_cast<uint32_t>(n_valid) * static_cast<uint32_t>(p.ldw);
-    const __amdgpu_buffer_rsrc_t wr0 = make_rsrc(w0 + static_cast<int64_t>(n0) * p.ldw, w_bytes);
+    const __amdgpu_buffer_rsrc_t wr0 =
+        make_rsrc(it.w0 + static_cast<int64_t>(n0) * p.ldw, w_bytes);
     const __amdgpu_buffer_rsrc_t wr1 =
-        kSwiglu ? make_rsrc(w1 + static_cast<int64_t>(n0) * p.ldw, w_bytes) : wr0;
-    // Rows: from the tile's first row, or (gathered) from row 0.
-    const bool gathered = kGrouped && p.gather != nullptr;
-    const int64_t a_base = gathered ? 0 : m0;
-    const int a_count = gathered ? p.a_rows : cnt;
-    const __amdgpu_buffer_rsrc_t ar =
-        make_rsrc(p.a + a_base * p.lda, static_cast<uint32_t>(a_count * p.lda));
-    const __amdgpu_buffer_rsrc_t sr =
-        make_rsrc(p.a_scale + a_base * p.ld_as, static_cast<uint32_t>(a_count * p.ld_as * 4));
-    // The source row of tile row r relative to the resources, -1 past the valid ones.
-    const auto src_row = [&](int r) {
-      if (r >= cnt) return -1;
-      if (!gathered) return r;
-      const int t = p.gather[m0 + r];
-      return t >= 0 && t < p.a_rows ? t : -1;
-    };
+        kSwiglu ? make_rsrc(it.w1 + static_cast<int64_t>(n0) * p.ldw, w_bytes) : wr0;
+    const Rows rows(p, it);
 
     // ---- this lane's load offsets: instruction i fills 8 LDS rows, lane l the physical
     // piece l % 8 of row l / 8, so it loads logical piece (l % 8) ^ (l / 8)
@@ -280,28 +487,23 @@ __global__ __launch_bounds__(C::kThreads) void fp8_gemm_kernel(const GemmArgs p)
 #pragma unroll
     for (int i = 0; i < C::kWLoads; ++i) {
       const int r = 8 * (sw * C::kWLoads + i) + (lane >> 3);
-      w_voff[i] = static_cast<uint32_t>(r & (kBnOut - 1)) * static_cast<uint32_t>(p.ldw) +
+      w_voff[i] = static_cast<uint32_t>(kSwiglu ? r % kBnOut : r) * static_cast<uint32_t>(p.ldw) +
                   16u * piece;
     }
 #pragma unroll
     for (int i = 0; i < C::kXLoads; ++i) {
       const int inst = sw * C::kXLoads + i;
-      const int r = inst < C::kXInstr ? src_row(8 * inst + (lane >> 3)) : -1;
+      const int r = inst < C::kXInstr ? rows.source(8 * inst + (lane >> 3)) : -1;
       x_voff[i] = r < 0 ? kNoLoad : static_cast<uint32_t>(r) * static_cast<uint32_t>(p.lda) +
                                         16u * piece;
     }
     {
       const int t = 64 * (sw % (C::kScaleFloats / 64)) + lane;
-      const int r = t < BT ? src_row(t) : -1;
+      const int r = t < BT ? rows.source(t) : -1;
       s_voff = r < 0 ? kNoLoad : static_cast<uint32_t>(r) * static_cast<uint32_t>(p.ld_as) * 4u;
     }
-    const auto dma_stage = [&](int j) {
-      const int kb = j * KS + slice;  // this wave's slice of the stage
-      // Bytes of this slice inside K; a piece past them is not loaded (zeros).
-      const int left = p.k - kb * kFp8Block;
-      const uint32_t dead = 16 * piece < left ? 0u : kNoLoad;
-      const int soff = left > 0 ? kb * kFp8Block : 0;
-      uint8_t *st = lds + (j % ST) * C::kStage + slice * C::kSlice;
+    const auto dma_masked = [&](int kb, uint8_t *st, uint32_t dead, uint32_t s_dead) {
+      const int soff = s_dead == 0 ? kb * kFp8Block : 0;
 #pragma unroll
       for (int i = 0; i < C::kWLoads; ++i) {
         const int row = 8 * (sw * C::kWLoads + i);
@@ -315,135 +517,223 @@ __global__ __launch_bounds__(C::kThreads) void fp8_gemm_kernel(const GemmArgs p)
         const int inst = sw * C::kXLoads + i;
         uint8_t *dst = inst < C::kXInstr ? st + C::kWBytes + inst * 1024 : lds + C::kDumpOff;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            ar, (__attribute__((address_space(3))) void *)dst, 16,
+            rows.codes, (__attribute__((address_space(3))) void *)dst, 16,
             static_cast<int>(x_voff[i] | dead), soff, 0, 0);
       }
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          sr,
+          rows.scales,
           (__attribute__((address_space(3))) void *)(st + C::kWBytes + C::kXBytes +
                                                      256 * (sw % (C::kScaleFloats / 64))),
-          4, static_cast<int>(s_voff | (left > 0 ? 0u : kNoLoad)), left > 0 ? 4 * kb : 0, 0, 0);
+          4, static_cast<int>(s_voff | s_dead), s_dead == 0 ? 4 * kb : 0, 0, 0);
+    };
+    const auto dma_stage = [&](int j, int stage_off) {
+      const int kb = kb0 + j * KS + slice;  // this wave's slice of the stage
+      uint8_t *st = lds + stage_off + slice * C::kSlice;
+      // Bytes of this slice inside K; a piece past them is not loaded (zeros).
+      const int left = kb < kb1 ? p.k - kb * kFp8Block : 0;
+      if (left >= kFp8Block) dma_masked(kb, st, 0u, 0u);  // wave-uniform
+      else dma_masked(kb, st, 16 * piece < left ? 0u : kNoLoad, left > 0 ? 0u : kNoLoad);
     };
 
+    WeightScales<C::kNBlocks, C::kThreads, kSwiglu> scales;
+    scales.load(p, it, kb_pad, tid);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < ST - 1; ++j) dma_stage(j);
+    for (int j = 0; j < ST - 1; ++j) dma_stage(j, j * C::kStage);
+    scales.store(sb, kb_pad, tid);
+    // Only the LDS stores are waited for here: the first step's barrier publishes them.
+    __builtin_amdgcn_s_waitcnt(kLgkmWaitImm);
 
-    // ---- the tile's weight scales for all of K
-    {
-      const int nb = (p.n + kFp8Block - 1) / kFp8Block;
-      for (int i = tid; i < C::kNBlocks * steps * KS; i += C::kThreads) {
-        const int blk = i / (steps * KS), kb = i - blk * (steps * KS);
-        float v = 0.0f;
-        if (kb < kb_n) {
-          if (kSwiglu)
-            v = (blk == 0 ? s0 : s1)[static_cast<int64_t>(n0 / kFp8Block) * kb_n + kb];
-          else if (n0 / kFp8Block + blk < nb)
-            v = s0[static_cast<int64_t>(n0 / kFp8Block + blk) * kb_n + kb];
-        }
-        sb[i] = v;
-      }
-      __syncthreads();
-    }
-
-    f32x4_t acc[NT][TT];
+    // acc[i][t][x]: output column w_row(i) + 4 gl + x of tile row kR (t WT + wt) + rl, with
+    // kR rows to a row tile and this lane's rl = lane % kR, gl = lane / kR.
+    constexpr int kR = C::kTileRows;
+    constexpr int kAN = kWide ? 8 : NT, kAT = kWide ? 2 : TT;
+    const int rl = lane % kR, gl = lane / kR;
+    f32x4_t acc[kAN][kAT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int i = 0; i < kAN; ++i)
 #pragma unroll
-      for (int t = 0; t < TT; ++t) acc[i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      for (int t = 0; t < kAT; ++t) acc[i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    // Weight tile i of this wave: its first LDS row and its scale row.
+    // LDS row (and output column) of acc[i]; in the wide form acc[4 j + q] holds columns 8 q of
+    // 32-row tile j. A wave of the SwiGLU form owns gate rows and the same up rows.
     const auto w_row = [&](int i) {
-      if (kSwiglu) return i < NT / 2 ? (wn * (NT / 2) + i) * 16 : kBnOut + (wn * (NT / 2) + i - NT / 2) * 16;
-      return (wn * NT + i) * 16;
+      constexpr int kHalf = kAN / 2, kStep = kWide ? 8 : 16;
+      if (kSwiglu) return (i < kHalf ? 0 : kBnOut) + (wn * kHalf + i % kHalf) * kStep;
+      return (wn * kAN + i) * kStep;
     };
-    const int frag = r16 * kRowBytes + 16 * (g4 ^ (r16 & 7));
+    // This wave's row tile t is tile t WT + wt; the tiles with rows are its first `live`.
+    const int live = max((cnt + kR - 1) / kR - wt + WT - 1, 0) / WT;
+    const int n_in_block = n0 % kFp8Block;
 
     constexpr int kWaitN = C::kLoads * (ST - 2);
     static_assert(ST >= 2 && kWaitN < 64, "vmcnt holds 6 bits");
     constexpr int kWaitImm = (kWaitN & 15) | ((kWaitN >> 4) << 14) | (7 << 4) | (15 << 8);
+    int cur = 0, fill = (ST - 1) * C::kStage;  // byte offsets of stages s and s + ST - 1
+    const auto next_stage = [](int off) { return off == (ST - 1) * C::kStage ? 0 : off + C::kStage; };
+    if constexpr (kWide) {
+      // Two phases per step and wave: read the step's operands (and convert them), then
+      // multiply. Waves 0-3 and 4-7 (one of each on every SIMD) run them in opposite order,
+      // the second group one barrier behind, so that a SIMD's matrix core is fed by one wave
+      // while the other loads. A stage's buffer is free again once both groups have read
+      // it, one phase before the first group's next loads into it.
+      using Wide = std::conditional_t<kSwiglu, Bf16Wide, Fp8Wide>;
+      int frag[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) frag[j] = rl * kRowBytes + 16 * ((2 * j + gl) ^ (rl & 7));
+      const auto read_wide = [&](const uint8_t *tile) {
+        WideCodes c;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          c.piece[j] = *reinterpret_cast<const u32x4_t *>(tile + frag[j]);
+        return c;
+      };
+      __builtin_amdgcn_s_waitcnt(kWaitImm);
+      __builtin_amdgcn_s_barrier();  // stage 0 has landed
+      if (wave >= 4) __builtin_amdgcn_s_barrier();
+      for (int s = 0; s < steps; ++s) {
+        dma_stage(s + ST - 1, fill);
+        fill = next_stage(fill);
+        const uint8_t *st = lds + cur;
+        cur = next_stage(cur);
+        const uint8_t *xs = st + C::kWBytes + wt * kR * kRowBytes;
+        const float *sa =
+            reinterpret_cast<const float *>(st + C::kWBytes + C::kXBytes) + wt * kR + rl;
+        float sbv[C::kNBlocks], sat[2];
+#pragma unroll
+        for (int b = 0; b < C::kNBlocks; ++b) sbv[b] = sb[b * kb_pad + kb0 + s];
+        sat[0] = sa[0];
+        sat[1] = sa[kR * WT];
+        typename Wide::Operand wf[2], xf[2];
+        wf[0] = Wide::operand(read_wide(st + w_row(0) * kRowBytes));
+        xf[0] = Wide::operand(read_wide(xs));
+        wf[1] = Wide::operand(read_wide(st + w_row(4) * kRowBytes));
+        xf[1] = Wide::operand(read_wide(xs + kR * WT * kRowBytes));
+        // The conversions belong to this phase: without a use here the compiler moves them
+        // into the other.
+#pragma unroll
+        for (int m = 0; m < Wide::kParts; ++m) {
+          asm volatile("" : "+v"(wf[0].part[m]), "+v"(xf[0].part[m]));
+          asm volatile("" : "+v"(wf[1].part[m]), "+v"(xf[1].part[m]));
+        }
+        __builtin_amdgcn_s_waitcnt(kWaitImm & kLgkmWaitImm);  // stage s + 1, and the reads
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (t < live) {  // wave-uniform
+            f32x16_t part[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+              for (int x = 0; x < 16; ++x) part[i][x] = 0.0f;
+#pragma unroll
+              for (int m = 0; m < Wide::kParts; ++m)
+                part[i] = Wide::mma(wf[i].part[m], xf[t].part[m], part[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float sbt = sbv[kSwiglu ? i : 0];
+              if constexpr (!kSwiglu && C::kNBlocks > 1)
+                sbt = n_in_block + w_row(4 * i) < kFp8Block ? sbv[0] : sbv[1];
+              const float sc = sat[t] * sbt;
+#pragma unroll
+              for (int x = 0; x < 16; ++x)
+                acc[4 * i + x / 4][t][x % 4] = fmaf(part[i][x], sc, acc[4 * i + x / 4][t][x % 4]);
+            }
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+      }
+      if (wave < 4) __builtin_amdgcn_s_barrier();
+    } else {
+    const int frag = r16 * kRowBytes + 16 * (g4 ^ (r16 & 7));
     for (int s = 0; s < steps; ++s) {
       __builtin_amdgcn_s_waitcnt(kWaitImm);  // this wave's loads of stage s are in LDS
       __builtin_amdgcn_s_barrier();           // every wave's; and stage s - 1 is read
-      dma_stage(s + ST - 1);                  // into stage s - 1's buffer
-      const uint8_t *st = lds + (s % ST) * C::kStage + slice * C::kSlice;
-      const uint8_t *xs = st + C::kWBytes + wt * TT * 16 * kRowBytes;
+      dma_stage(s + ST - 1, fill);            // into stage s - 1's buffer
+      const uint8_t *st = lds + cur + slice * C::kSlice;
+      cur = next_stage(cur);
+      fill = next_stage(fill);
+      const uint8_t *xs = st + C::kWBytes + wt * 16 * kRowBytes;
       const float *sa =
-          reinterpret_cast<const float *>(st + C::kWBytes + C::kXBytes) + wt * TT * 16 + r16;
+          reinterpret_cast<const float *>(st + C::kWBytes + C::kXBytes) + wt * 16 + r16;
       float sbv[C::kNBlocks];
 #pragma unroll
-      for (int b = 0; b < C::kNBlocks; ++b) sbv[b] = sb[b * steps * KS + s * KS + slice];
-      typename Mma::Operand wf[NT];
+      for (int b = 0; b < C::kNBlocks; ++b) sbv[b] = sb[b * kb_pad + kb0 + s * KS + slice];
+      if (live == 0) continue;  // wave-uniform; the loop ends with no barrier of its own
+      // Row tile t's products are issued with tile t + 1's LDS reads before them and tile
+      // t - 1's FMAs behind them, so that neither waits; the weights are converted between
+      // the first tile's products.
+      Codes xc = read_codes(xs, frag), wc[NT];
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
-        wf[i] = Mma::operand(read_codes(st + w_row(i) * kRowBytes, frag));
+      for (int i = 0; i < NT; ++i) wc[i] = read_codes(st + w_row(i) * kRowBytes, frag);
+      float sat[TT];
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const typename Mma::Operand xf =
-            Mma::operand(read_codes(xs + t * 16 * kRowBytes, frag));
-        const float sat = sa[16 * t];
+      for (int t = 0; t < TT; ++t) sat[t] = sa[16 * WT * t];
+      typename Mma::Operand wf[NT], xf = Mma::operand(xc);
+      f32x4_t part[2][NT];
+      const auto add = [&](int t) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          const f32x4_t part = Mma::product(wf[i], xf);
-          const int blk = kSwiglu ? (i < NT / 2 ? 0 : 1) : 0;
-          float sbt;
+          float sbt = sbv[kSwiglu && i >= NT / 2 ? 1 : 0];
           if constexpr (!kSwiglu && C::kNBlocks > 1)
-            sbt = w_row(i) < kFp8Block ? sbv[0] : sbv[1];  // wave-uniform
-          else
-            sbt = sbv[blk];
-          const float sc = sat * sbt;
+            sbt = n_in_block + w_row(i) < kFp8Block ? sbv[0] : sbv[1];  // wave-uniform
+          const float sc = sat[t] * sbt;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) acc[i][t][x] = fmaf(part[x], sc, acc[i][t][x]);
+          for (int x = 0; x < 4; ++x) acc[i][t][x] = fmaf(part[t & 1][i][x], sc, acc[i][t][x]);
         }
-      }
+      };
+      const auto tile = [&](auto self, auto index) __attribute__((always_inline)) -> void {
+        constexpr int t = decltype(index)::value;
+        if constexpr (t + 1 < TT) xc = read_codes(xs + (t + 1) * WT * 16 * kRowBytes, frag);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          if (t == 0) wf[i] = Mma::operand(wc[i]);
+          part[t & 1][i] = Mma::product(wf[i], xf);
+          if (t == 0 && kSwiglu) __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (t > 0) add(t - 1);
+        if constexpr (t + 1 < TT) {
+          if (t + 1 < live) {  // wave-uniform
+            xf = Mma::operand(xc);
+            __builtin_amdgcn_sched_barrier(0);
+            self(self, std::integral_constant<int, t + 1>{});
+          } else {
+            add(t);
+          }
+        } else {
+          add(t);
+        }
+      };
+      tile(tile, std::integral_constant<int, 0>{});
+    }
     }
     // The past-the-end stages' loads write LDS (zeros) too: they finish first.
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();  // every wave's operand reads are done: the stages are free
 
-    // ---- epilogue: acc[i][t][x] is output column w_row(i) + 4 g4 + x of tile row
-    // (wt TT + t) 16 + r16
+    // ---- epilogue
     if constexpr (kSwiglu) {
-      constexpr int kH = NT / 2;
-      constexpr int kRow = kFp8Block + 16;  // staged code row, padded
-      float *red = reinterpret_cast<float *>(lds + BT * kRow);  // [WN][BT] magnitudes
-      static_assert(BT * kRow + WN * BT * 4 + BT * 4 <= C::kDumpOff, "epilogue fits the stages");
+      static_assert(swiglu_epilogue_bytes(BT, WN) <= C::kDumpOff, "epilogue fits the stages");
+      if (p.partial != nullptr) {  // uniform: this split's sums, for the finishing kernel
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        uint32_t m = 0;
+        for (int t = 0; t < kAT; ++t) {
+          const int r = kR * (t * WT + wt) + rl;
+          if (r >= cnt) continue;
+          float *row = p.partial +
+                       ((static_cast<int64_t>(split) * p.rows + m0 + r) * 2) * p.n + n0 + 4 * gl;
 #pragma unroll
-        for (int i = 0; i < kH; ++i)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const bool in = w_row(i) + 4 * g4 + x < n_valid;
-            const float v = moe::swiglu_clamp1(acc[i][t][x], acc[i + kH][t][x], p.limit);
-            acc[i][t][x] = v;
-            if (in) m = max(m, __float_as_uint(v) & 0x7FFFFFFFu);
+          for (int i = 0; i < kAN; ++i) {
+            const int col = w_row(i) % kBnOut;
+            if (col < n_valid)
+              *reinterpret_cast<f32x4_t *>(row + (i < kAN / 2 ? 0 : p.n) + col) = acc[i][t];
           }
-        m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16, 64)));
-        m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32, 64)));
-        if (g4 == 0) red[wn * BT + (wt * TT + t) * 16 + r16] = __uint_as_float(m);
-      }
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int r = (wt * TT + t) * 16 + r16;
-        uint32_t m = 0;
-#pragma unroll
-        for (int w = 0; w < WN; ++w) m = max(m, __float_as_uint(red[w * BT + r]));
-        const float s = moe::fp8_scale(m);
-        if (wn == 0 && g4 == 0 && r < cnt)
-          p.q_scale[static_cast<int64_t>(m0 + r) * p.ld_qs + n0 / kFp8Block] = s;
-#pragma unroll
-        for (int i = 0; i < kH; ++i)
-          *reinterpret_cast<uint32_t *>(lds + r * kRow + w_row(i) + 4 * g4) =
-              moe::e4m3x4(acc[i][t][0] / s, acc[i][t][1] / s, acc[i][t][2] / s, acc[i][t][3] / s);
-      }
-      __syncthreads();
-      for (int u = tid; u < BT * (kFp8Block / 16); u += C::kThreads) {
-        const int r = u / (kFp8Block / 16), ch = u % (kFp8Block / 16);
-        if (r >= cnt || ch * 16 >= n_valid) continue;
-        *reinterpret_cast<u32x4_t *>(p.q + static_cast<int64_t>(m0 + r) * p.ldc + n0 + ch * 16) =
-            *reinterpret_cast<const u32x4_t *>(lds + r * kRow + ch * 16);
+        }
+      } else {
+        swiglu_epilogue<kAN, kAT, kR, WN, BT, C::kThreads>(
+            p, it, lds, acc, w_row, [&](int t) { return t * WT + wt; }, wn, tid);
       }
     } else if constexpr (KS > 1) {
       // The slice groups' sums, joined in slice order.
@@ -451,11 +741,11 @@ __global__ __launch_bounds__(C::kThreads) void fp8_gemm_kernel(const GemmArgs p)
       static_assert(KS * BT * kRow * 4 <= C::kDumpOff, "epilogue fits the stages");
       float *red = reinterpret_cast<float *>(lds);
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < kAN; ++i)
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-          *reinterpret_cast<f32x4_t *>(red + (slice * BT + (wt * TT + t) * 16 + r16) * kRow +
-                                       w_row(i) + 4 * g4) = acc[i][t];
+        for (int t = 0; t < kAT; ++t)
+          *reinterpret_cast<f32x4_t *>(red + (slice * BT + kR * (t * WT + wt) + rl) * kRow +
+                                       w_row(i) + 4 * gl) = acc[i][t];
       __syncthreads();
       for (int u = tid; u < BT * (BN / 4); u += C::kThreads) {
         const int r = u / (BN / 4), q = u % (BN / 4);
@@ -473,14 +763,14 @@ __global__ __launch_bounds__(C::kThreads) void fp8_gemm_kernel(const GemmArgs p)
       constexpr int kRow = 2 * BN + 16;  // bytes
       static_assert(BT * kRow <= C::kDumpOff, "epilogue fits the stages");
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < kAN; ++i)
 #pragma unroll
-        for (int t = 0; t < TT; ++t) {
+        for (int t = 0; t < kAT; ++t) {
           uint2 o;
           o.x = moe::pack_bf16x2(acc[i][t][0], acc[i][t][1]);
           o.y = moe::pack_bf16x2(acc[i][t][2], acc[i][t][3]);
-          *reinterpret_cast<uint2 *>(lds + ((wt * TT + t) * 16 + r16) * kRow +
-                                     2 * (w_row(i) + 4 * g4)) = o;
+          *reinterpret_cast<uint2 *>(lds + (kR * (t * WT + wt) + rl) * kRow +
+                                     2 * (w_row(i) + 4 * gl)) = o;
         }
       __syncthreads();
       for (int u = tid; u < BT * (BN / 8); u += C::kThreads) {
@@ -494,9 +784,64 @@ __global__ __launch_bounds__(C::kThreads) void fp8_gemm_kernel(const GemmArgs p)
   }
 }
 
+// The split-K SwiGLU form's second launch: 32 lanes own a row's 128 columns, sum the splits'
+// FP32 sums in split order, apply the SwiGLU and quantise. Grouped: rows that no present
+// expert covers are left alone.
+constexpr int kFinishThreads = 256;
+
+template <bool kGrouped>
+__global__ __launch_bounds__(kFinishThreads) void fp8_swiglu_finish_kernel(GemmArgs p) {
+  const int nb = (p.n + kFp8Block - 1) / kFp8Block;
+  const int64_t grp = static_cast<int64_t>(blockIdx.x) * (kFinishThreads / 32) + threadIdx.x / 32;
+  const int64_t row = grp / nb;
+  if (row >= p.rows) return;  // whole 32-lane groups leave together
+  const int blk = static_cast<int>(grp - row * nb), sub = threadIdx.x % 32;
+  if constexpr (kGrouped) {
+    // The last expert whose first row is at most `row`, by halving [lo, hi).
+    int lo = 0, hi = p.num_experts;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (p.offsets[mid] <= row) lo = mid;
+      else hi = mid;
+    }
+    if (p.w_ptrs[lo] == 0 || row < p.offsets[lo] || row >= p.offsets[lo + 1]) return;
+  }
+  const int col = blk * kFp8Block + 4 * sub;
+  const bool live = col < p.n;
+  f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+  if (live) {
+    const float *src = p.partial + row * 2 * p.n + col;
+    const int64_t way = static_cast<int64_t>(p.rows) * 2 * p.n;
+    f32x4_t g = *reinterpret_cast<const f32x4_t *>(src);
+    f32x4_t u = *reinterpret_cast<const f32x4_t *>(src + p.n);
+    for (int w = 1; w < p.ways; ++w) {
+      g += *reinterpret_cast<const f32x4_t *>(src + w * way);
+      u += *reinterpret_cast<const f32x4_t *>(src + w * way + p.n);
+    }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = moe::swiglu_clamp1(g[x], u[x], p.limit);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) m = max(m, __float_as_uint(v[x]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1)
+    m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), d, 32)));
+  const float s = moe::fp8_scale(m);
+  if (sub == 0) p.q_scale[row * p.ld_qs + blk] = s;
+  if (live)
+    *reinterpret_cast<uint32_t *>(p.q + row * p.ldc + col) =
+        moe::e4m3x4(v[0] / s, v[1] / s, v[2] / s, v[3] / s);
+}
+
 // ------------------------------------------------------------------------------- host
 
 constexpr int kMaxDevices = 64;
+
+int current_device() {
+  int device = 0;
+  return hipGetDevice(&device) == hipSuccess ? device : -1;
+}
 
 // Compute units of the current device (the persistent grid's size), looked up once each.
 int compute_units(int device) {
@@ -515,8 +860,8 @@ int compute_units(int device) {
 }
 
 // Raises the kernel's dynamic LDS limit once per device.
-template <class Kern>
-bool allow_lds(Kern kern, int device) {
+template <void (*kern)(GemmArgs)>
+bool allow_lds(int device) {
   static std::mutex mu;
   static bool done[kMaxDevices] = {};
   std::lock_guard<std::mutex> lock(mu);
@@ -528,43 +873,132 @@ bool allow_lds(Kern kern, int device) {
   return true;
 }
 
-template <class C, bool kSwiglu, bool kGrouped>
-int run(const char *name, const GemmArgs &p, void *stream) {
-  int device = 0;
-  if (hipGetDevice(&device) != hipSuccess) device = -1;
-  const auto kern = fp8_gemm_kernel<C, kSwiglu, kGrouped>;
-  const int bytes = lds_bytes<C, kGrouped>(p);
-  if (!allow_lds(kern, device)) {
+// A persistent launch of `kern` over tiles of bt rows x bn_out output columns.
+template <void (*kern)(GemmArgs)>
+int run_tiles(const char *name, int bytes, int threads, int bt, int bn_out, bool grouped,
+              const GemmArgs &p, void *stream) {
+  const int device = current_device();
+  if (!allow_lds<kern>(device)) {
     moe::set_error("%s: the device refuses %d bytes of LDS", name, bytes);
     return MOE_ELAUNCH;
   }
-  const int bn_out = kSwiglu ? C::BN / 2 : C::BN;
   const int64_t n_tiles = (p.n + bn_out - 1) / bn_out;
   // Most row tiles there can be: every expert's last tile may be partial.
   const int64_t row_tiles =
-      kGrouped ? static_cast<int64_t>(p.rows) / C::BT +
-                     (p.num_experts < p.rows ? p.num_experts : p.rows)
-               : (static_cast<int64_t>(p.rows) + C::BT - 1) / C::BT;
+      grouped ? static_cast<int64_t>(p.rows) / bt +
+                    (p.num_experts < p.rows ? p.num_experts : p.rows)
+              : (static_cast<int64_t>(p.rows) + bt - 1) / bt;
   const int64_t per_cu = 160 * 1024 / bytes;
   const int64_t resident = (per_cu < 1 ? 1 : per_cu) * compute_units(device);
-  const int64_t grid = row_tiles * n_tiles < resident ? row_tiles * n_tiles : resident;
-  return moe::launch(name, kern, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), bytes,
+  const int64_t items = row_tiles * n_tiles * p.ways;
+  const int64_t grid = items < resident ? items : resident;
+  return moe::launch(name, kern, dim3(static_cast<unsigned>(grid)), dim3(threads), bytes,
                      stream, p);
 }
 
-// Tiles: rows per item from the (average) rows there are.
+template <class C, bool kSwiglu, bool kGrouped>
+int run(const char *name, const GemmArgs &p, void *stream) {
+  return run_tiles<fp8_gemm_kernel<C, kSwiglu, kGrouped>>(
+      name, lds_bytes<C, kGrouped>(p), C::kThreads, C::BT, kSwiglu ? C::BN / 2 : C::BN, kGrouped, p, stream);
+}
+
+// The tiles a launch can take, narrowest first: weight rows x rows per tile.
+//   plain   128 x 32   128 x 64   256 x 128 (two-phase)   32 x 16, four slice groups
+//   SwiGLU  256 x 32   256 x 64   256 x 128 (two-phase)
+constexpr int kTileRowsOf[4] = {32, 64, 128, 16};
+constexpr int kPlainWidthOf[4] = {128, 128, 256, 32};
+
+struct Plan {
+  int tile, ways;
+};
+
+// Which tile, and how many splits of K (SwiGLU with a workspace only): the least of an
+// estimate in microseconds, from two measured rates. A CU takes in about 0.32 MB/us
+// (0.0031 us per LDS row of 128 bytes; 64 KB in flight and any tile shape end there), so a
+// step costs 0.0031 us x (weight rows + rows); the SwiGLU form's conversions and BF16 products
+// cost 0.0205 us per row and step (0.0151 in the two-phase loop), the FP8 products stay below
+// the loads. An item costs 2 us more (its first loads), a launch 4. A split adds a launch (6
+// with its wait) and writes and reads its sums, at 2.5 and 4 TB/s. HBM bounds all of it:
+// experts' weights / 6 TB/s. At equal estimates the earlier tile is taken (two blocks of it
+// fit a CU, so that one loads while the other starts).
+template <bool kSwiglu>
+Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, int cus) {
+  const double used = experts > 0 ? static_cast<double>(experts < rows ? experts : rows) : 1.0;
+  const double avg = static_cast<double>(rows) / used;
+  const int64_t kb = (k + kFp8Block - 1) / kFp8Block;
+  const double weights = used * static_cast<double>(n) * static_cast<double>(k) * (kSwiglu ? 2 : 1);
+  Plan best = {0, 1};
+  double best_us = 1e30;
+  for (int t = 0; t < (kSwiglu ? 3 : 4); ++t) {
+    const int bt = kTileRowsOf[t];
+    const int width = kSwiglu ? 2 * kFp8Block : kPlainWidthOf[t];
+    const int bn_out = kSwiglu ? kFp8Block : width;
+    // Row tiles per expert: exact for one matrix; for experts of `avg` rows on average, one
+    // where they seldom pass the tile, else half a tile more than the rows need.
+    double tiles = experts > 0 ? (avg <= 0.75 * bt ? 1.0 : avg / bt + 0.5)
+                               : static_cast<double>((rows + bt - 1) / bt);
+    if (tiles > avg) tiles = avg;
+    const double live = experts > 0 ? avg / tiles : (avg < bt ? avg : bt);
+    double step = 0.0031 * (width + live);
+    if (kSwiglu) {
+      const double compute = (t == 2 ? 0.0151 : 0.0205) * live;
+      if (compute > step) step = compute;
+    }
+    const double items = used * tiles * static_cast<double>((n + bn_out - 1) / bn_out);
+    for (int ways = 1; ways <= (kSwiglu && split ? 8 : 1); ways *= 2) {
+      if (ways > 1 && (items * ways > 1.5 * cus || kb < 3 * ways)) break;
+      double rounds = static_cast<double>(static_cast<int64_t>((items * ways + cus - 1) / cus));
+      if (rounds < 1.0) rounds = 1.0;
+      double us = rounds * (static_cast<double>((kb + ways - 1) / ways) * step + 2.0);
+      if (us < weights / 6e6) us = weights / 6e6;
+      if (ways > 1)
+        us += 6.0 + static_cast<double>(ways) * rows * n * 8.0 * (1.0 / 2.5e6 + 1.0 / 4e6);
+      if (us < best_us) {
+        best_us = us;
+        best = {t, ways};
+      }
+    }
+  }
+  return best;
+}
+
+int64_t partial_bytes(const Plan &plan, int64_t rows, int64_t n) {
+  return plan.ways > 1 ? plan.ways * rows * n * 8 : 0;
+}
+
 template <bool kSwiglu, bool kGrouped>
-int dispatch(const char *name, const GemmArgs &p, void *stream) {
-  int64_t avg = p.rows;
-  if (kGrouped) avg = p.rows / (p.num_experts < p.rows ? p.num_experts : p.rows);
+int dispatch(const char *name, GemmArgs p, void *workspace, int64_t workspace_bytes,
+             void *stream) {
+  const Plan plan = plan_for<kSwiglu>(p.rows, kGrouped ? p.num_experts : 0, p.n, p.k,
+                                      workspace != nullptr, compute_units(current_device()));
+  p.ways = plan.ways;
   if constexpr (kSwiglu) {
-    if (avg <= 12) return run<Cfg<2, 2, 8, 1, 1, 2>, kSwiglu, kGrouped>(name, p, stream);
-    if (avg <= 40) return run<Cfg<2, 4, 8, 1, 1, 3>, kSwiglu, kGrouped>(name, p, stream);
-    return run<Cfg<2, 8, 8, 1, 1, 3>, kSwiglu, kGrouped>(name, p, stream);
+    if (plan.ways > 1) {
+      const int64_t need = partial_bytes(plan, p.rows, p.n);
+      MOE_REQUIRE_CODE(workspace_bytes >= need, MOE_ECAPACITY,
+                       "%s: a workspace of %lld bytes, these sizes need %lld", name,
+                       static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+      p.partial = static_cast<float *>(workspace);
+    }
+    int rc;
+    switch (plan.tile) {
+      case 0: rc = run<Cfg<2, 2, 8, 1, 1, 2>, true, kGrouped>(name, p, stream); break;
+      case 1: rc = run<Cfg<4, 2, 4, 2, 1, 3>, true, kGrouped>(name, p, stream); break;
+      default: rc = run<Cfg<4, 4, 4, 2, 1, 3, true>, true, kGrouped>(name, p, stream); break;
+    }
+    if (rc != MOE_OK || plan.ways == 1) return rc;
+    const int64_t groups = static_cast<int64_t>(p.rows) * ((p.n + kFp8Block - 1) / kFp8Block);
+    constexpr int kPer = kFinishThreads / 32;
+    return moe::launch(name, fp8_swiglu_finish_kernel<kGrouped>,
+                       dim3(static_cast<unsigned>((groups + kPer - 1) / kPer)),
+                       dim3(kFinishThreads), 0, stream, p);
   } else {
-    if (avg <= 12) return run<Cfg<2, 2, 4, 1, 1, 3>, kSwiglu, kGrouped>(name, p, stream);
-    if (avg <= 40) return run<Cfg<2, 4, 4, 1, 1, 3>, kSwiglu, kGrouped>(name, p, stream);
-    return run<Cfg<2, 8, 8, 1, 1, 3>, kSwiglu, kGrouped>(name, p, stream);
+    switch (plan.tile) {
+      case 0: return run<Cfg<2, 2, 4, 1, 1, 3>, false, kGrouped>(name, p, stream);
+      case 1: return run<Cfg<4, 2, 2, 2, 1, 3>, false, kGrouped>(name, p, stream);
+      case 2: return run<Cfg<4, 4, 4, 2, 1, 3, true>, false, kGrouped>(name, p, stream);
+      default: return run<Cfg<2, 1, 1, 1, 4, 3>, false, kGrouped>(name, p, stream);
+    }
   }
 }
 
@@ -584,7 +1018,13 @@ int check_common(const char *name, const GemmArgs &p) {
               name);
   MOE_REQUIRE(p.ld_as >= (p.k + kFp8Block - 1) / kFp8Block && p.ld_as < (1 << 20),
               "%s: ld_a_scale must be >= ceil(k / 128) and below 2^20", name);
-  MOE_REQUIRE(p.rows >= 0, "%s: the row count must be >= 0", name);
+  MOE_REQUIRE(p.rows >= 0 && p.rows <= (1 << 30), "%s: the row count must be in [0, 2^30]", name);
+  return MOE_OK;
+}
+
+int check_workspace(const char *name, const void *workspace) {
+  MOE_REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0,
+              "%s: the workspace must be 256-byte aligned", name);
   return MOE_OK;
 }
 
@@ -659,7 +1099,7 @@ extern "C" int moe_dense_gemm_fp8(const uint8_t *a, int64_t lda, const float *a_
   p.c = c, p.ldc = ldc, p.rows = m, p.n = n, p.k = k;
   const int rc = check_dense("dense_gemm_fp8", p, false);
   if (rc != MOE_OK || m == 0) return rc;
-  return dispatch<false, false>("moe_dense_gemm_fp8", p, stream);
+  return dispatch<false, false>("moe_dense_gemm_fp8", p, nullptr, 0, stream);
 }
 
 extern "C" int moe_dense_gate_up_swiglu_fp8(const uint8_t *a, int64_t lda, const float *a_scale,
@@ -668,16 +1108,20 @@ extern "C" int moe_dense_gate_up_swiglu_fp8(const uint8_t *a, int64_t lda, const
                                             const float *up_scale, int64_t ldw, uint8_t *act,
                                             int64_t ld_act, float *act_scale,
                                             int64_t ld_act_scale, int32_t m, int32_t inter,
-                                            int32_t k, float limit, void *stream) {
+                                            int32_t k, float limit,
+                                            void *workspace, int64_t workspace_bytes,
+                                            void *stream) {
   moe::clear_error();
   GemmArgs p = {};
   p.a = a, p.lda = lda, p.a_scale = a_scale, p.ld_as = ld_a_scale, p.a_rows = m;
   p.w0 = gate_w, p.w1 = up_w, p.ldw = ldw, p.ws0 = gate_scale, p.ws1 = up_scale;
   p.q = act, p.ldc = ld_act, p.q_scale = act_scale, p.ld_qs = ld_act_scale;
   p.rows = m, p.n = inter, p.k = k, p.limit = limit;
-  const int rc = check_dense("dense_gate_up_swiglu_fp8", p, true);
+  int rc = check_dense("dense_gate_up_swiglu_fp8", p, true);
+  if (rc == MOE_OK) rc = check_workspace("dense_gate_up_swiglu_fp8", workspace);
   if (rc != MOE_OK || m == 0) return rc;
-  return dispatch<true, false>("moe_dense_gate_up_swiglu_fp8", p, stream);
+  return dispatch<true, false>("moe_dense_gate_up_swiglu_fp8", p, workspace, workspace_bytes,
+                               stream);
 }
 
 extern "C" int moe_w8a8_grouped_gemm(const uint8_t *a, int64_t lda, const float *a_scale,
@@ -694,7 +1138,7 @@ extern "C" int moe_w8a8_grouped_gemm(const uint8_t *a, int64_t lda, const float 
   p.c = c, p.ldc = ldc, p.rows = max_rows, p.n = n, p.k = k;
   const int rc = check_grouped("w8a8_grouped_gemm", p, false);
   if (rc != MOE_OK || max_rows == 0) return rc;
-  return dispatch<false, true>("moe_w8a8_grouped_gemm", p, stream);
+  return dispatch<false, true>("moe_w8a8_grouped_gemm", p, nullptr, 0, stream);
 }
 
 extern "C" int moe_w8a8_grouped_gemm_swiglu(
@@ -702,7 +1146,7 @@ extern "C" int moe_w8a8_grouped_gemm_swiglu(
     const int32_t *a_gather, const uint64_t *weight_ptrs, const uint64_t *scale_ptrs,
     const int32_t *expert_offsets, int32_t num_experts, uint8_t *act, int64_t ld_act,
     float *act_scale, int64_t ld_act_scale, int32_t max_rows, int32_t mi, int32_t k, float limit,
-    void *stream) {
+    void *workspace, int64_t workspace_bytes, void *stream) {
   moe::clear_error();
   GemmArgs p = {};
   p.a = a, p.lda = lda, p.a_scale = a_scale, p.ld_as = ld_a_scale, p.a_rows = a_rows;
@@ -710,7 +1154,17 @@ extern "C" int moe_w8a8_grouped_gemm_swiglu(
   p.offsets = expert_offsets, p.num_experts = num_experts;
   p.q = act, p.ldc = ld_act, p.q_scale = act_scale, p.ld_qs = ld_act_scale;
   p.rows = max_rows, p.n = mi, p.k = k, p.limit = limit;
-  const int rc = check_grouped("w8a8_grouped_gemm_swiglu", p, true);
+  int rc = check_grouped("w8a8_grouped_gemm_swiglu", p, true);
+  if (rc == MOE_OK) rc = check_workspace("w8a8_grouped_gemm_swiglu", workspace);
   if (rc != MOE_OK || max_rows == 0) return rc;
-  return dispatch<true, true>("moe_w8a8_grouped_gemm_swiglu", p, stream);
+  return dispatch<true, true>("moe_w8a8_grouped_gemm_swiglu", p, workspace, workspace_bytes,
+                              stream);
+}
+
+extern "C" int64_t moe_fp8_swiglu_workspace_bytes(int32_t rows, int32_t num_experts,
+                                                  int32_t width, int32_t k) {
+  if (rows <= 0 || num_experts < 0 || width <= 0 || k <= 0) return 0;
+  const Plan plan =
+      plan_for<true>(rows, num_experts, width, k, true, compute_units(current_device()));
+  return partial_bytes(plan, rows, width);
 }

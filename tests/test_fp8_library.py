@@ -62,18 +62,20 @@ def test_dense(lib):
 
 def test_dense_swiglu(lib):
     base = dict(a=_p(), lda=512, sa=_p(), lds=4, g=_p(), sg=_p(), u=_p(), su=_p(), ldw=512,
-                act=_p(), ld_act=272, os=_p(), ld_os=3, m=0, n=272, k=512, limit=7.0)
+                act=_p(), ld_act=272, os=_p(), ld_os=3, m=0, n=272, k=512, limit=7.0, ws=N, wb=0)
 
     def call(**kw):
         a = {**base, **kw}
         return lib.moe_dense_gate_up_swiglu_fp8(
             a["a"], a["lda"], a["sa"], a["lds"], a["g"], a["sg"], a["u"], a["su"], a["ldw"],
-            a["act"], a["ld_act"], a["os"], a["ld_os"], a["m"], a["n"], a["k"], a["limit"], N)
+            a["act"], a["ld_act"], a["os"], a["ld_os"], a["m"], a["n"], a["k"], a["limit"],
+            a["ws"], a["wb"], N)
     assert call() == 0
     for kw in (dict(limit=0.0), dict(limit=-1.0), dict(limit=float("nan")), dict(ld_act=264),
                dict(ld_act=280), dict(ld_os=2), dict(n=264), dict(m=2, g=N), dict(m=2, u=N),
                dict(m=2, sg=N), dict(m=2, su=N), dict(m=2, act=N), dict(m=2, os=N),
-               dict(m=2, act=_p(0x1008)), dict(m=2, u=_p(0x1004)), dict(ldw=500)):
+               dict(m=2, act=_p(0x1008)), dict(m=2, u=_p(0x1004)), dict(ldw=500),
+               dict(ws=_p(0x1010), wb=1 << 30)):
         assert call(**kw) == 1, kw
         assert lib.moe_w4a16_last_error().startswith(b"dense_gate_up_swiglu_fp8")
 
@@ -81,7 +83,7 @@ def test_dense_swiglu(lib):
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_grouped(lib, swiglu):
     base = dict(a=_p(), lda=512, sa=_p(), lds=4, a_rows=8, g=N, wp=_p(), sp=_p(), off=_p(), e=4,
-                out=_p(), ldo=272, os=_p(), ld_os=3, rows=0, n=272, k=512, limit=7.0)
+                out=_p(), ldo=272, os=_p(), ld_os=3, rows=0, n=272, k=512, limit=7.0, ws=N, wb=0)
 
     def call(**kw):
         a = {**base, **kw}
@@ -89,7 +91,7 @@ def test_grouped(lib, swiglu):
                 a["off"], a["e"], a["out"], a["ldo"])
         if swiglu:
             return lib.moe_w8a8_grouped_gemm_swiglu(*head, a["os"], a["ld_os"], a["rows"], a["n"],
-                                                    a["k"], a["limit"], N)
+                                                    a["k"], a["limit"], a["ws"], a["wb"], N)
         return lib.moe_w8a8_grouped_gemm(*head, a["rows"], a["n"], a["k"], N)
     assert call() == 0
     for kw in (dict(rows=-1), dict(e=0), dict(e=2049), dict(a_rows=-1), dict(rows=4, a_rows=0),
@@ -99,3 +101,13 @@ def test_grouped(lib, swiglu):
                dict(rows=4, g=_p(), a_rows=1 << 20, lds=1 << 10)):
         assert call(**kw) == 1, kw
         assert b"w8a8_grouped_gemm" in lib.moe_w4a16_last_error()
+
+
+def test_swiglu_workspace_query(lib):
+    for rows, width, k in ((1, 2048, 6144), (256, 2048, 6144), (16, 512, 2048)):
+        need = lib.moe_fp8_swiglu_workspace_bytes(rows, 0, width, k)
+        ways = need // (rows * width * 8)  # FP32 gate and up sums per split
+        assert ways in (2, 4, 8) and need == ways * rows * width * 8
+    for args in ((0, 0, 2048, 6144), (-1, 0, 64, 64), (4, -1, 64, 64), (4, 0, 0, 64),
+                 (4, 0, 64, 0), (4096, 0, 2048, 6144), (2048, 256, 2048, 6144), (1, 0, 64, 128)):
+        assert lib.moe_fp8_swiglu_workspace_bytes(*args) == 0, args

@@ -278,6 +278,61 @@ def test_dense_swiglu(hip, m, n, k):
     assert np.array_equal(_host8(q2), _host8(q)) and torch.equal(s2, s)
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 2048, 6144), (8, 272, 2048), (40, 144, 2064),
+                                   (200, 400, 2064)])
+def test_dense_swiglu_split_over_k(hip, m, n, k):
+    """Sizes that split K: through a workspace of the caller's, through the call's own (same
+    bits), nothing written past it, and a workspace that is too small is refused."""
+    need = hip.moe_fp8_swiglu_workspace_bytes(m, 0, n, k)
+    assert need > 0 and need % (m * n * 8) == 0
+    rng = np.random.default_rng(m + n)
+    a, sa = _normal_operand(rng, m, k, False)
+    gate, up = (_normal_operand(rng, n, k, True) for _ in range(2))
+    gate, up = (gate[0], gate[1] * 448 * 4), (up[0], up[1] * 448 * 4)
+    args = (_f8(a), _dev(sa), _f8(gate[0]), _dev(gate[1]), _f8(up[0]), _dev(up[1]))
+    qb, q = _out8(m, n)
+    sb, s = _outs(m, n)
+    buf = torch.full((need + 512,), 0x6B, dtype=torch.uint8, device="cuda")
+    hip.moe_dense_gate_up_swiglu_fp8(*args, q, s, 7.0, workspace=buf[:need])
+    ref = fp8.swiglu_product(a, sa, gate, up, 7.0)
+    _assert_quantised(_host8(q), s.cpu().numpy(), ref, _swiglu_rel(a, sa, gate, up, ref, 7.0))
+    assert bool(torch.all(buf[need:] == 0x6B))
+    assert _rest_is(qb, POISON8, m, n) and _rest_is(sb, -7.0, m, fp8.blocks(n))
+    q2, s2 = torch.empty((m, n), dtype=q.dtype, device="cuda"), torch.empty_like(s)
+    hip.moe_dense_gate_up_swiglu_fp8(*args, q2, s2, 7.0)
+    assert np.array_equal(_host8(q2), _host8(q)) and torch.equal(s2, s)
+    q2.view(torch.uint8).fill_(POISON8)
+    with pytest.raises(hip.MoeError) as err:
+        hip.moe_dense_gate_up_swiglu_fp8(*args, q2, s2, 7.0, workspace=buf[:need - 16])
+    assert err.value.status == 2
+    torch.cuda.synchronize()
+    assert bool(torch.all(q2.view(torch.uint8) == POISON8))
+
+
+def test_dense_swiglu_split_on_another_stream(hip):
+    """The call's own workspace belongs to the given stream: two chains on two streams."""
+    rng = np.random.default_rng(31)
+    m, n, k = 16, 512, 2048
+    assert hip.moe_fp8_swiglu_workspace_bytes(m, 0, n, k) > 0
+    jobs = []
+    for _ in range(2):
+        a, sa = _normal_operand(rng, m, k, False)
+        g, u = (_normal_operand(rng, n, k, True) for _ in range(2))
+        args = (_f8(a), _dev(sa), _f8(g[0]), _dev(g[1]), _f8(u[0]), _dev(u[1]))
+        outs = [(torch.empty((m, n), dtype=torch.float8_e4m3fn, device="cuda"),
+                 torch.empty((m, fp8.blocks(n)), device="cuda")) for _ in range(2)]
+        hip.moe_dense_gate_up_swiglu_fp8(*args, *outs[0], 7.0)
+        jobs.append((args, outs, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for args, outs, st in jobs:
+            hip.moe_dense_gate_up_swiglu_fp8(*args, *outs[1], 7.0, stream=st)
+    torch.cuda.synchronize()
+    for _, outs, _ in jobs:
+        assert np.array_equal(_host8(outs[0][0]), _host8(outs[1][0]))
+        assert torch.equal(outs[0][1], outs[1][1])
+
+
 def _swiglu_rel(a, sa, gate, up, ref, limit):
     """The largest error of v = silu(G) U in FP32, relative to its group's largest |v|: the
     sums' errors times the partial derivatives (|silu'| <= 1.1, |U| <= limit, |silu(G)| <=
@@ -320,7 +375,7 @@ GROUPED = [  # experts, rows, n, k, counts
     (1, 1, 16, 16, "even"), (4, 3, 272, 144, "even"), (9, 21, 272, 656, "skew"),
     (16, 130, 144, 512, "even"), (16, 513, 400, 272, "skew"), (64, 100, 256, 256, "skew"),
     (70, 2000, 128, 400, "skew"), (8, 700, 1040, 528, "even"), (130, 260, 160, 128, "even"),
-    (3, 1500, 272, 1040, "skew"), (2048, 300, 32, 48, "even")]
+    (3, 1500, 272, 1040, "skew"), (2048, 300, 32, 48, "even"), (5, 1100, 528, 400, "even")]
 
 
 @pytest.mark.parametrize("experts,rows,n,k,kind", GROUPED)
@@ -384,7 +439,7 @@ def test_grouped_offsets_that_are_no_prefix_sum_stay_in_range(hip, off):
 GROUPED_SWIGLU = [  # experts, tokens, top_k, mi, k, counts
     (1, 1, 1, 16, 16, "even"), (8, 3, 2, 128, 272, "even"), (9, 33, 3, 272, 656, "skew"),
     (16, 65, 4, 144, 512, "even"), (16, 300, 4, 400, 272, "skew"), (64, 20, 8, 256, 256, "skew"),
-    (4, 500, 2, 272, 1040, "skew")]
+    (4, 500, 2, 272, 1040, "skew"), (6, 400, 3, 160, 400, "even"), (40, 900, 2, 144, 272, "skew")]
 
 
 @pytest.mark.parametrize("experts,tokens,top_k,mi,k,kind", GROUPED_SWIGLU)
@@ -422,6 +477,35 @@ def test_grouped_swiglu(hip, experts, tokens, top_k, mi, k, kind):
             src = (src[0][live], src[1][live])
             _assert_quantised(codes[lo:hi][live], scale[lo:hi][live], ref[live],
                               _swiglu_rel(*src, gate, up, ref[live], limit))
+    assert _rest_is(qb, POISON8, rows, mi, written)
+    assert _rest_is(sb, -7.0, rows, fp8.blocks(mi), written)
+
+
+def test_grouped_swiglu_split_leaves_uncovered_rows(hip):
+    """The split form's second launch writes the rows of present experts only."""
+    rng = np.random.default_rng(33)
+    experts, rows, mi, k = 6, 24, 144, 2064
+    off = _offsets([5, 0, 4, 6, 2, 3])  # rows 20.. belong to nobody
+    assert hip.moe_fp8_swiglu_workspace_bytes(rows, experts, mi, k) > 0
+    a, sa = _normal_operand(rng, rows, k, False)
+    weights = []
+    for e in range(experts):
+        g, u = (_normal_operand(rng, mi, k, True) for _ in range(2))
+        weights.append(None if e in (2, 5) else (np.concatenate([g[0], u[0]]),
+                                                 np.concatenate([g[1], u[1]]) * np.float32(448)))
+    qb, q = _out8(rows, mi)
+    sb, s = _outs(rows, mi)
+    hip.moe_w8a8_grouped_gemm_swiglu(_f8(a), _dev(sa), _table(hip, weights, 2 * mi, k, True),
+                                     _dev(off), q, s, 7.0)
+    written = np.zeros(rows, bool)
+    for e, lo, hi in fp8.segments(off, rows):
+        if weights[e] is None:
+            continue
+        written[lo:hi] = True
+        gate, up = fp8.split_gate_up(*weights[e])
+        ref = fp8.swiglu_product(a[lo:hi], sa[lo:hi], gate, up, 7.0)
+        _assert_quantised(_host8(q)[lo:hi], s.cpu().numpy()[lo:hi], ref,
+                          _swiglu_rel(a[lo:hi], sa[lo:hi], gate, up, ref, 7.0))
     assert _rest_is(qb, POISON8, rows, mi, written)
     assert _rest_is(sb, -7.0, rows, fp8.blocks(mi), written)
 
