@@ -81,6 +81,14 @@ struct GemmArgs {
   int32_t ways;             // splits of K (1: none)
 };
 
+// One stage's loads of a wave: its K block, scalar offset, offset bits for what lies past K, and
+// its slice in LDS.
+struct StageLoads {
+  int kb, soff;
+  uint32_t dead, s_dead;
+  uint8_t *st;
+};
+
 // Compile-time shape of a kernel: NT 16-row weight tiles and TT 16-row row tiles per wave,
 // WN x WT waves over the tile, KS slice groups, ST stages. kWide: 32 x 32 products in the
 // two-phase loop.
@@ -88,8 +96,8 @@ template <int NT_, int TT_, int WN_, int WT_, int KS_, int ST_, bool kWide_ = fa
 struct Cfg {
   static constexpr bool kWide = kWide_;
   static constexpr int kTileRows = kWide ? 32 : 16;  // rows of a row tile
-  static_assert(!kWide || (NT_ == 4 && TT_ == 4 && WN_ * WT_ == 8 && KS_ == 1 && ST_ >= 3),
-                "the two-phase loop: 64 x 64 per wave");
+  static_assert(!kWide || (NT_ == 4 && TT_ == 4 && WN_ * WT_ == 8 && KS_ == 1 && ST_ == 3),
+                "the two-phase loop: 64 x 64 per wave, three stages");
   static constexpr int NT = NT_, TT = TT_, WN = WN_, WT = WT_, KS = KS_, ST = ST_;
   static constexpr int BN = 16 * NT * WN, BT = 16 * TT * WT;
   static constexpr int kSliceWaves = WN * WT;
@@ -111,6 +119,8 @@ struct Cfg {
   static_assert(BN % 64 == 0 || kFp8Block % BN == 0, "a tile's rows lie in kNBlocks blocks");
   // LDS: stages, a dump for loads that must not land anywhere, weight scales, tile prefix
   static constexpr int kDumpOff = ST * kStage;
+  // Waves per SIMD the registers leave room for: as many as the LDS does, two blocks at most.
+  static constexpr int kMinWaves = kStage * ST <= 80 * 1024 - 6144 ? kWaves / 2 : kWaves / 4;
   static constexpr int kSbOff = kDumpOff + 1024;
 };
 
@@ -170,6 +180,12 @@ struct Bf16Mma {
   }
 };
 
+// A use of `v` here, so that what computes it is not moved further down.
+template <class T>
+__device__ __forceinline__ void keep(T &v) {
+  asm volatile("" : "+v"(v));
+}
+
 // The same for 32 x 32 x 128 block products (half the matrix instructions per output). A lane
 // holds 64 codes of a row, two lanes per row.
 struct WideCodes {
@@ -181,14 +197,11 @@ struct Fp8Wide {
     i32x8_t part[2];
   };
   static constexpr int kParts = 2;
-  static __device__ __forceinline__ Operand operand(const WideCodes &c) {
-    Operand o;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      o.part[j] = __builtin_bit_cast(
-          i32x8_t, __builtin_shufflevector(c.piece[2 * j], c.piece[2 * j + 1], 0, 1, 2, 3, 4, 5,
-                                           6, 7));
-    return o;
+  // Part j of the operand.
+  static __device__ __forceinline__ void convert(const WideCodes &c, Operand &o, int j) {
+    o.part[j] = __builtin_bit_cast(
+        i32x8_t,
+        __builtin_shufflevector(c.piece[2 * j], c.piece[2 * j + 1], 0, 1, 2, 3, 4, 5, 6, 7));
   }
   static __device__ __forceinline__ f32x16_t mma(const i32x8_t &w, const i32x8_t &x, f32x16_t d) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, d, 0, 0, 0, 0, 0, 0);
@@ -200,20 +213,24 @@ struct Bf16Wide {
     bf16x8_t part[8];
   };
   static constexpr int kParts = 8;
-  static __device__ __forceinline__ Operand operand(const WideCodes &c) {
-    Operand o;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      o.part[2 * j] = Bf16Mma::eight(c.piece[j][0], c.piece[j][1]);
-      o.part[2 * j + 1] = Bf16Mma::eight(c.piece[j][2], c.piece[j][3]);
-    }
-    return o;
+  static __device__ __forceinline__ void convert(const WideCodes &c, Operand &o, int j) {
+    o.part[j] = Bf16Mma::eight(c.piece[j / 2][2 * (j % 2)], c.piece[j / 2][2 * (j % 2) + 1]);
   }
   static __device__ __forceinline__ f32x16_t mma(const bf16x8_t &w, const bf16x8_t &x,
                                                  f32x16_t d) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, x, d, 0, 0, 0);
   }
 };
+
+// A wave-uniform pointer as the compiler sees one (in scalar registers): buffer resources made
+// from a pointer it takes for divergent are read lane by lane at every load.
+template <class T>
+__device__ __forceinline__ const T *uniform(const T *ptr) {
+  const uint64_t u = reinterpret_cast<uint64_t>(ptr);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(u >> 32));
+  return reinterpret_cast<const T *>(static_cast<uint64_t>(hi) << 32 | lo);
+}
 
 // One unit of work: rows [m0, m0 + cnt) of expert (or matrix) w0 / w1 and output columns
 // [n0, n0 + n_valid).
@@ -271,7 +288,7 @@ struct Items {
         const int e = base + lane;
         below += __popcll(__ballot(e < p.num_experts && prefix[e] <= ty));
       }
-      const int e = max(below - 1, 0);
+      const int e = __builtin_amdgcn_readfirstlane(max(below - 1, 0));
       lo = max(p.offsets[e], 0);
       hi = min(p.offsets[e + 1], p.rows);
       local = item - static_cast<int64_t>(__builtin_amdgcn_readfirstlane(prefix[e])) * n_tiles;
@@ -334,8 +351,8 @@ struct Rows {
       : gather(p.gather != nullptr ? p.gather + it.m0 : nullptr), cnt(it.cnt), a_rows(p.a_rows) {
     const int64_t base = gather != nullptr ? 0 : it.m0;
     const int64_t rows = gather != nullptr ? p.a_rows : it.cnt;
-    codes = make_rsrc(p.a + base * p.lda, static_cast<uint32_t>(rows * p.lda));
-    scales = make_rsrc(p.a_scale + base * p.ld_as, static_cast<uint32_t>(rows * p.ld_as * 4));
+    codes = make_rsrc(uniform(p.a + base * p.lda), static_cast<uint32_t>(rows * p.lda));
+    scales = make_rsrc(uniform(p.a_scale + base * p.ld_as), static_cast<uint32_t>(rows * p.ld_as * 4));
   }
 
   // Row of the resources that tile row r reads, -1 for zeros.
@@ -439,8 +456,7 @@ int lds_bytes(const GemmArgs &p) {
 }
 
 template <class C, bool kSwiglu, bool kGrouped>
-__global__ __launch_bounds__(C::kThreads) __attribute__((amdgpu_waves_per_eu(2, 4))) void
-fp8_gemm_kernel(GemmArgs p) {
+__global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(GemmArgs p) {
   static_assert(!kSwiglu || (C::BN == 2 * kFp8Block && C::KS == 1 && C::NT % 2 == 0),
                 "the SwiGLU form owns whole output groups");
   constexpr int NT = C::NT, TT = C::TT, WN = C::WN, WT = C::WT, KS = C::KS, ST = C::ST;
@@ -474,10 +490,11 @@ fp8_gemm_kernel(GemmArgs p) {
     const int steps = max(kb1 - kb0 + KS - 1, 0) / KS;
     const int n0 = it.n0, n_valid = it.n_valid, m0 = it.m0, cnt = it.cnt;
     const uint32_t w_bytes = static_cast<uint32_t>(n_valid) * static_cast<uint32_t>(p.ldw);
-    const __amdgpu_buffer_rsrc_t wr0 =
-        make_rsrc(it.w0 + static_cast<int64_t>(n0) * p.ldw, w_bytes);
-    const __amdgpu_buffer_rsrc_t wr1 =
-        kSwiglu ? make_rsrc(it.w1 + static_cast<int64_t>(n0) * p.ldw, w_bytes) : wr0;
+    // The weight this wave loads: its rows of the tile lie in one half (SwiGLU: gate or up).
+    static_assert(!kSwiglu || kBnOut / 8 % C::kWLoads == 0, "a wave loads rows of one half");
+    const uint8_t *w_src = kSwiglu && 8 * sw * C::kWLoads >= kBnOut ? it.w1 : it.w0;
+    const __amdgpu_buffer_rsrc_t wr =
+        make_rsrc(uniform(w_src + static_cast<int64_t>(n0) * p.ldw), w_bytes);
     const Rows rows(p, it);
 
     // ---- this lane's load offsets: instruction i fills 8 LDS rows, lane l the physical
@@ -502,44 +519,53 @@ fp8_gemm_kernel(GemmArgs p) {
       const int r = t < BT ? rows.source(t) : -1;
       s_voff = r < 0 ? kNoLoad : static_cast<uint32_t>(r) * static_cast<uint32_t>(p.ld_as) * 4u;
     }
-    const auto dma_masked = [&](int kb, uint8_t *st, uint32_t dead, uint32_t s_dead) {
-      const int soff = s_dead == 0 ? kb * kFp8Block : 0;
-#pragma unroll
-      for (int i = 0; i < C::kWLoads; ++i) {
-        const int row = 8 * (sw * C::kWLoads + i);
+    // A stage's loads: kWLoads of weights, kXLoads of rows, one of row scales, issued singly
+    // with piece(n): a wave's loads queue behind the other waves' (a CU takes in 1 KB in about
+    // 28 cycles), so they are spread between the step's other work.
+    const auto stage_loads = [&](int j, int stage_off) {
+      StageLoads g;
+      g.kb = kb0 + j * KS + slice;  // this wave's slice of the stage
+      g.st = lds + stage_off + slice * C::kSlice;
+      // Bytes of this slice inside K; a piece past them is not loaded (zeros).
+      const int left = g.kb < kb1 ? p.k - g.kb * kFp8Block : 0;
+      g.dead = 16 * piece < left ? 0u : kNoLoad;
+      g.s_dead = left > 0 ? 0u : kNoLoad;
+      g.soff = left > 0 ? g.kb * kFp8Block : 0;
+      return g;
+    };
+    const auto load_piece = [&](const StageLoads &g, int n) __attribute__((always_inline)) {
+      if (n < C::kWLoads) {
+        const int row = 8 * (sw * C::kWLoads + n);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            kSwiglu && row >= kBnOut ? wr1 : wr0,
-            (__attribute__((address_space(3))) void *)(st + row * kRowBytes), 16,
-            static_cast<int>(w_voff[i] | dead), soff, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < C::kXLoads; ++i) {
-        const int inst = sw * C::kXLoads + i;
-        uint8_t *dst = inst < C::kXInstr ? st + C::kWBytes + inst * 1024 : lds + C::kDumpOff;
+            wr, (__attribute__((address_space(3))) void *)(g.st + row * kRowBytes), 16,
+            static_cast<int>(w_voff[n < C::kWLoads ? n : 0] | g.dead), g.soff, 0, 0);
+      } else if (n < C::kWLoads + C::kXLoads) {
+        const int i = n - C::kWLoads, inst = sw * C::kXLoads + i;
+        uint8_t *dst = inst < C::kXInstr ? g.st + C::kWBytes + inst * 1024 : lds + C::kDumpOff;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rows.codes, (__attribute__((address_space(3))) void *)dst, 16,
-            static_cast<int>(x_voff[i] | dead), soff, 0, 0);
+            static_cast<int>(x_voff[i] | g.dead), g.soff, 0, 0);
+      } else {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rows.scales,
+            (__attribute__((address_space(3))) void *)(g.st + C::kWBytes + C::kXBytes +
+                                                       256 * (sw % (C::kScaleFloats / 64))),
+            4, static_cast<int>(s_voff | g.s_dead), g.s_dead == 0 ? 4 * g.kb : 0, 0, 0);
       }
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rows.scales,
-          (__attribute__((address_space(3))) void *)(st + C::kWBytes + C::kXBytes +
-                                                     256 * (sw % (C::kScaleFloats / 64))),
-          4, static_cast<int>(s_voff | s_dead), s_dead == 0 ? 4 * kb : 0, 0, 0);
     };
-    const auto dma_stage = [&](int j, int stage_off) {
-      const int kb = kb0 + j * KS + slice;  // this wave's slice of the stage
-      uint8_t *st = lds + stage_off + slice * C::kSlice;
-      // Bytes of this slice inside K; a piece past them is not loaded (zeros).
-      const int left = kb < kb1 ? p.k - kb * kFp8Block : 0;
-      if (left >= kFp8Block) dma_masked(kb, st, 0u, 0u);  // wave-uniform
-      else dma_masked(kb, st, 16 * piece < left ? 0u : kNoLoad, left > 0 ? 0u : kNoLoad);
+    // Loads [from * kLoads / of, to * kLoads / of) of a stage.
+    const auto load_part = [&](const StageLoads &g, int from, int to, int of)
+        __attribute__((always_inline)) {
+#pragma unroll
+      for (int n = 0; n < C::kLoads; ++n)
+        if (n >= from * C::kLoads / of && n < to * C::kLoads / of) load_piece(g, n);
     };
 
     WeightScales<C::kNBlocks, C::kThreads, kSwiglu> scales;
     scales.load(p, it, kb_pad, tid);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < ST - 1; ++j) dma_stage(j, j * C::kStage);
+    for (int j = 0; j < ST - 1; ++j) load_part(stage_loads(j, j * C::kStage), 0, 1, 1);
     scales.store(sb, kb_pad, tid);
     // Only the LDS stores are waited for here: the first step's barrier publishes them.
     __builtin_amdgcn_s_waitcnt(kLgkmWaitImm);
@@ -572,11 +598,15 @@ fp8_gemm_kernel(GemmArgs p) {
     int cur = 0, fill = (ST - 1) * C::kStage;  // byte offsets of stages s and s + ST - 1
     const auto next_stage = [](int off) { return off == (ST - 1) * C::kStage ? 0 : off + C::kStage; };
     if constexpr (kWide) {
-      // Two phases per step and wave: read the step's operands (and convert them), then
-      // multiply. Waves 0-3 and 4-7 (one of each on every SIMD) run them in opposite order,
-      // the second group one barrier behind, so that a SIMD's matrix core is fed by one wave
-      // while the other loads. A stage's buffer is free again once both groups have read
-      // it, one phase before the first group's next loads into it.
+      // Two phases per step and wave: read the step's operands (and convert the first ones),
+      // then multiply. Waves 0-3 and 4-7 (one of each on every SIMD) run them in opposite
+      // order, the second group one barrier behind, so that a SIMD's matrix core is fed by one
+      // wave while the other reads. The loads of later stages are issued between the products.
+      // In slots between barriers, step s is read in slot 2 s by the first group and 2 s + 1 by
+      // the second, and multiplied in the slot after: in its products of step s the second
+      // group finds the buffer of stage s free (it loads stage s + ST into it), the first only
+      // that of stage s - 1 (stage s + ST - 1). A stage has landed when both groups have
+      // waited for it, at the end of the products that issue the loads after it.
       using Wide = std::conditional_t<kSwiglu, Bf16Wide, Fp8Wide>;
       int frag[4];
 #pragma unroll
@@ -588,71 +618,92 @@ fp8_gemm_kernel(GemmArgs p) {
           c.piece[j] = *reinterpret_cast<const u32x4_t *>(tile + frag[j]);
         return c;
       };
+      const int group = wave / 4;
+      if (group == 1) load_part(stage_loads(ST - 1, fill), 0, 1, 1);
       __builtin_amdgcn_s_waitcnt(kWaitImm);
-      __builtin_amdgcn_s_barrier();  // stage 0 has landed
-      if (wave >= 4) __builtin_amdgcn_s_barrier();
-      for (int s = 0; s < steps; ++s) {
-        dma_stage(s + ST - 1, fill);
-        fill = next_stage(fill);
-        const uint8_t *st = lds + cur;
-        cur = next_stage(cur);
-        const uint8_t *xs = st + C::kWBytes + wt * kR * kRowBytes;
-        const float *sa =
-            reinterpret_cast<const float *>(st + C::kWBytes + C::kXBytes) + wt * kR + rl;
-        float sbv[C::kNBlocks], sat[2];
+      __builtin_amdgcn_s_barrier();  // stage 0 (the second group's part of stage 1 too)
+      if (group == 1) __builtin_amdgcn_s_barrier();
+      // kTiles: this item's row tiles per wave (two unless it has at most 64 rows).
+      const auto loop = [&](auto tiles) __attribute__((always_inline)) {
+        constexpr int kTiles = decltype(tiles)::value;
+        for (int s = 0; s < steps; ++s) {
+          const StageLoads loads = stage_loads(s + ST - 1 + group, group == 1 ? cur : fill);
+          fill = next_stage(fill);
+          const uint8_t *st = lds + cur;
+          cur = next_stage(cur);
+          const uint8_t *xs = st + C::kWBytes + wt * kR * kRowBytes;
+          const float *sa =
+              reinterpret_cast<const float *>(st + C::kWBytes + C::kXBytes) + wt * kR + rl;
+          float sbv[C::kNBlocks], sat[kTiles];
+          WideCodes codes[2 + kTiles];  // two weight tiles, then the row tiles
+          codes[0] = read_wide(st + w_row(0) * kRowBytes);
+          codes[1] = read_wide(st + w_row(4) * kRowBytes);
 #pragma unroll
-        for (int b = 0; b < C::kNBlocks; ++b) sbv[b] = sb[b * kb_pad + kb0 + s];
-        sat[0] = sa[0];
-        sat[1] = sa[kR * WT];
-        typename Wide::Operand wf[2], xf[2];
-        wf[0] = Wide::operand(read_wide(st + w_row(0) * kRowBytes));
-        xf[0] = Wide::operand(read_wide(xs));
-        wf[1] = Wide::operand(read_wide(st + w_row(4) * kRowBytes));
-        xf[1] = Wide::operand(read_wide(xs + kR * WT * kRowBytes));
-        // The conversions belong to this phase: without a use here the compiler moves them
-        // into the other.
+          for (int t = 0; t < kTiles; ++t) codes[2 + t] = read_wide(xs + kR * WT * t * kRowBytes);
 #pragma unroll
-        for (int m = 0; m < Wide::kParts; ++m) {
-          asm volatile("" : "+v"(wf[0].part[m]), "+v"(xf[0].part[m]));
-          asm volatile("" : "+v"(wf[1].part[m]), "+v"(xf[1].part[m]));
-        }
-        __builtin_amdgcn_s_waitcnt(kWaitImm & kLgkmWaitImm);  // stage s + 1, and the reads
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
+          for (int b = 0; b < C::kNBlocks; ++b) sbv[b] = sb[b * kb_pad + kb0 + s];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (t < live) {  // wave-uniform
-            f32x16_t part[2];
+          for (int t = 0; t < kTiles; ++t) sat[t] = sa[kR * WT * t];
+          __builtin_amdgcn_sched_barrier(0);
+          // This phase converts the first weight tile and row tile; the products convert the
+          // others beside them.
+          typename Wide::Operand wf[2], xf[kTiles];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-              for (int x = 0; x < 16; ++x) part[i][x] = 0.0f;
-#pragma unroll
-              for (int m = 0; m < Wide::kParts; ++m)
-                part[i] = Wide::mma(wf[i].part[m], xf[t].part[m], part[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float sbt = sbv[kSwiglu ? i : 0];
-              if constexpr (!kSwiglu && C::kNBlocks > 1)
-                sbt = n_in_block + w_row(4 * i) < kFp8Block ? sbv[0] : sbv[1];
-              const float sc = sat[t] * sbt;
-#pragma unroll
-              for (int x = 0; x < 16; ++x)
-                acc[4 * i + x / 4][t][x % 4] = fmaf(part[i][x], sc, acc[4 * i + x / 4][t][x % 4]);
-            }
+          for (int m = 0; m < Wide::kParts; ++m) {
+            Wide::convert(codes[0], wf[0], m);
+            Wide::convert(codes[2], xf[0], m);
+            // A use here: otherwise the compiler moves the conversions to the products.
+            keep(wf[0].part[m]);
+            keep(xf[0].part[m]);
+            __builtin_amdgcn_sched_barrier(0);
           }
+          __builtin_amdgcn_s_waitcnt(kLgkmWaitImm);  // every read of the stage is done
+          __builtin_amdgcn_s_barrier();
+          __builtin_amdgcn_sched_barrier(0);
+          // Product q = 2 t + i of weight tile i and row tile t, its FMAs under the next one.
+          f32x16_t part[2];
+          const auto add = [&](int q, int m) __attribute__((always_inline)) {  // its m-th share
+            const int i = q & 1, t = q >> 1;
+            float sbt = sbv[kSwiglu ? i : 0];
+            if constexpr (!kSwiglu && C::kNBlocks > 1)
+              sbt = n_in_block + w_row(4 * i) < kFp8Block ? sbv[0] : sbv[1];
+            const float sc = sat[t] * sbt;
+#pragma unroll
+            for (int x = m * 16 / Wide::kParts; x < (m + 1) * 16 / Wide::kParts; ++x)
+              acc[4 * i + x / 4][t][x % 4] =
+                  fmaf(part[q & 1][x], sc, acc[4 * i + x / 4][t][x % 4]);
+          };
+#pragma unroll
+          for (int q = 0; q < 2 * kTiles; ++q) {
+            f32x16_t d = {};
+#pragma unroll
+            for (int m = 0; m < Wide::kParts; ++m) {
+              d = Wide::mma(wf[q & 1].part[m], xf[q >> 1].part[m], d);
+              if (q == 0) Wide::convert(codes[1], wf[1], m);
+              if (q == 1 && kTiles > 1) Wide::convert(codes[kTiles + 1], xf[kTiles - 1], m);
+              if (q > 0) add(q - 1, m);
+              load_part(loads, q * Wide::kParts + m, q * Wide::kParts + m + 1,
+                        2 * kTiles * Wide::kParts);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+            part[q & 1] = d;
+          }
+#pragma unroll
+          for (int m = 0; m < Wide::kParts; ++m) add(2 * kTiles - 1, m);
+          __builtin_amdgcn_s_waitcnt(kWaitImm);  // all but the loads just issued have landed
+          __builtin_amdgcn_sched_barrier(0);
+          __builtin_amdgcn_s_barrier();
         }
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_barrier();
-      }
-      if (wave < 4) __builtin_amdgcn_s_barrier();
+      };
+      if (cnt > kR * WT) loop(std::integral_constant<int, 2>{});
+      else loop(std::integral_constant<int, 1>{});
+      if (group == 0) __builtin_amdgcn_s_barrier();
     } else {
     const int frag = r16 * kRowBytes + 16 * (g4 ^ (r16 & 7));
     for (int s = 0; s < steps; ++s) {
       __builtin_amdgcn_s_waitcnt(kWaitImm);  // this wave's loads of stage s are in LDS
       __builtin_amdgcn_s_barrier();           // every wave's; and stage s - 1 is read
-      dma_stage(s + ST - 1, fill);            // into stage s - 1's buffer
+      load_part(stage_loads(s + ST - 1, fill), 0, 1, 1);  // into stage s - 1's buffer
       const uint8_t *st = lds + cur + slice * C::kSlice;
       cur = next_stage(cur);
       fill = next_stage(fill);
@@ -859,9 +910,9 @@ int compute_units(int device) {
   return cus[device];
 }
 
-// Raises the kernel's dynamic LDS limit once per device.
-template <void (*kern)(GemmArgs)>
-bool allow_lds(int device) {
+// Raises the dynamic LDS limit of the kernel of configuration Key once per device.
+template <class Key>
+bool allow_lds(void (*kern)(GemmArgs), int device) {
   static std::mutex mu;
   static bool done[kMaxDevices] = {};
   std::lock_guard<std::mutex> lock(mu);
@@ -873,33 +924,32 @@ bool allow_lds(int device) {
   return true;
 }
 
-// A persistent launch of `kern` over tiles of bt rows x bn_out output columns.
-template <void (*kern)(GemmArgs)>
-int run_tiles(const char *name, int bytes, int threads, int bt, int bn_out, bool grouped,
-              const GemmArgs &p, void *stream) {
+template <class C, bool kSwiglu, bool kGrouped>
+struct Key {};
+
+// A persistent launch of one configuration.
+template <class C, bool kSwiglu, bool kGrouped>
+int run(const char *name, const GemmArgs &p, void *stream) {
+  void (*const kern)(GemmArgs) = fp8_gemm_kernel<C, kSwiglu, kGrouped>;
   const int device = current_device();
-  if (!allow_lds<kern>(device)) {
+  const int bytes = lds_bytes<C, kGrouped>(p);
+  if (!allow_lds<Key<C, kSwiglu, kGrouped>>(kern, device)) {
     moe::set_error("%s: the device refuses %d bytes of LDS", name, bytes);
     return MOE_ELAUNCH;
   }
+  const int bn_out = kSwiglu ? C::BN / 2 : C::BN;
   const int64_t n_tiles = (p.n + bn_out - 1) / bn_out;
   // Most row tiles there can be: every expert's last tile may be partial.
   const int64_t row_tiles =
-      grouped ? static_cast<int64_t>(p.rows) / bt +
-                    (p.num_experts < p.rows ? p.num_experts : p.rows)
-              : (static_cast<int64_t>(p.rows) + bt - 1) / bt;
+      kGrouped ? static_cast<int64_t>(p.rows) / C::BT +
+                     (p.num_experts < p.rows ? p.num_experts : p.rows)
+               : (static_cast<int64_t>(p.rows) + C::BT - 1) / C::BT;
   const int64_t per_cu = 160 * 1024 / bytes;
   const int64_t resident = (per_cu < 1 ? 1 : per_cu) * compute_units(device);
   const int64_t items = row_tiles * n_tiles * p.ways;
   const int64_t grid = items < resident ? items : resident;
-  return moe::launch(name, kern, dim3(static_cast<unsigned>(grid)), dim3(threads), bytes,
+  return moe::launch(name, kern, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), bytes,
                      stream, p);
-}
-
-template <class C, bool kSwiglu, bool kGrouped>
-int run(const char *name, const GemmArgs &p, void *stream) {
-  return run_tiles<fp8_gemm_kernel<C, kSwiglu, kGrouped>>(
-      name, lds_bytes<C, kGrouped>(p), C::kThreads, C::BT, kSwiglu ? C::BN / 2 : C::BN, kGrouped, p, stream);
 }
 
 // The tiles a launch can take, narrowest first: weight rows x rows per tile.
@@ -917,10 +967,12 @@ struct Plan {
 // (0.0031 us per LDS row of 128 bytes; 64 KB in flight and any tile shape end there), so a
 // step costs 0.0031 us x (weight rows + rows); the SwiGLU form's conversions and BF16 products
 // cost 0.0205 us per row and step (0.0151 in the two-phase loop), the FP8 products stay below
-// the loads. An item costs 2 us more (its first loads), a launch 4. A split adds a launch (6
-// with its wait) and writes and reads its sums, at 2.5 and 4 TB/s. HBM bounds all of it:
-// experts' weights / 6 TB/s. At equal estimates the earlier tile is taken (two blocks of it
-// fit a CU, so that one loads while the other starts).
+// the loads. An item costs 2 us more (its first loads), 0.7 where two blocks fit a CU and one
+// loads while the other starts. A split adds a launch (6 with its wait) and writes and reads
+// its sums, at 2.5 and 4 TB/s. HBM bounds all of it (the experts' weights at 6 TB/s); a tenth
+// of the estimate stands for what does not run beside that. Checked where tiles meet: 256
+// experts, gate/up width 2048 x K 6144, 8 rows each 1065 us with 32-row tiles and 1100 with
+// 64; 32 rows each 1485 and 1237; 128 rows each 2858 with 64-row tiles and 2490 with 128.
 template <bool kSwiglu>
 Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, int cus) {
   const double used = experts > 0 ? static_cast<double>(experts < rows ? experts : rows) : 1.0;
@@ -949,8 +1001,10 @@ Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, i
       if (ways > 1 && (items * ways > 1.5 * cus || kb < 3 * ways)) break;
       double rounds = static_cast<double>(static_cast<int64_t>((items * ways + cus - 1) / cus));
       if (rounds < 1.0) rounds = 1.0;
-      double us = rounds * (static_cast<double>((kb + ways - 1) / ways) * step + 2.0);
-      if (us < weights / 6e6) us = weights / 6e6;
+      const bool two_fit = kSwiglu ? t == 0 : t != 2;
+      double us = rounds * (static_cast<double>((kb + ways - 1) / ways) * step +
+                            (two_fit ? 0.7 : 2.0));
+      us = 0.1 * us + (us < weights / 6e6 ? weights / 6e6 : us);
       if (ways > 1)
         us += 6.0 + static_cast<double>(ways) * rows * n * 8.0 * (1.0 / 2.5e6 + 1.0 / 4e6);
       if (us < best_us) {
