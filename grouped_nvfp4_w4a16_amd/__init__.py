@@ -193,7 +193,7 @@ def _stream(stream):
     import torch
 
     if stream is None:  # the current stream's handle, without making a Stream object
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -654,25 +654,28 @@ def _fp8_matrix(t, name):
     """Leading dimension of a row-major 2-D device tensor of E4M3 codes."""
     import torch
 
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-        raise TypeError(f"{name}: expected E4M3 codes (float8_e4m3fn or uint8), got {t.dtype}")
-    if t.dim() != 2 or t.stride(1) != 1 or not t.is_cuda:
+    dtype = t.dtype
+    if dtype != torch.float8_e4m3fn and dtype != torch.uint8:
+        raise TypeError(f"{name}: expected E4M3 codes (float8_e4m3fn or uint8), got {dtype}")
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1 or not t.is_cuda:
         raise ValueError(f"{name}: expected a row-major 2-D device tensor")
-    return t.stride(0)
+    return stride[0]
 
 
 def _scale_matrix(t, rows, cols, name, contiguous=False):
     """Leading dimension of a float32 [rows, cols] device tensor (at least)."""
     import torch
 
-    if t.dtype != torch.float32 or t.dim() != 2 or not t.is_cuda:
+    shape, stride = t.shape, t.stride()
+    if t.dtype != torch.float32 or len(stride) != 2 or not t.is_cuda:
         raise TypeError(f"{name}: expected a 2-D float32 device tensor")
-    if t.shape[0] < rows or t.shape[1] < cols or (cols > 1 and t.stride(1) != 1):
+    if shape[0] < rows or shape[1] < cols or (cols > 1 and stride[1] != 1):
         raise ValueError(f"{name}: needs {rows} x {cols} scales, rows contiguous")
-    if contiguous and (t.shape[1] != cols or not t.is_contiguous()):
+    if contiguous and (shape[1] != cols or not t.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous [{rows}, {cols}] tensor")
     # of a single row the stride says nothing
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+    return stride[0] if shape[0] > 1 else max(stride[0], cols)
 
 
 def _fp8_blocks(n):
@@ -683,9 +686,9 @@ def _same_device(*tensors):
     """Raises unless every tensor lies on the current device (the launch goes there)."""
     import torch
 
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor lies on {t.device}, the current device is cuda:{dev}")
 
 
@@ -710,8 +713,8 @@ def moe_dense_gemm_fp8(a, a_scale, b, b_scale, c, stream=None) -> None:
     lda, ldb = _fp8_matrix(a, "a"), _fp8_matrix(b, "b")
     c, ldc = _bf16_matrix(c, "c")
     m, k = a.shape
-    n = b.shape[0]
-    if b.shape[1] != k or tuple(c.shape) != (m, n):
+    n, kw = b.shape
+    if kw != k or c.shape != (m, n):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, "
                          f"c {tuple(c.shape)}")
     kb = _fp8_blocks(k)
