@@ -714,6 +714,41 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
 #pragma unroll
       for (int b = 0; b < C::kNBlocks; ++b) sbv[b] = sb[b * kb_pad + kb0 + s * KS + slice];
       if (live == 0) continue;  // wave-uniform; the loop ends with no barrier of its own
+      const auto scale_of = [&](int i) {
+        if constexpr (!kSwiglu && C::kNBlocks > 1)
+          return n_in_block + w_row(i) < kFp8Block ? sbv[0] : sbv[1];  // wave-uniform
+        else
+          return sbv[kSwiglu && i >= NT / 2 ? 1 : 0];
+      };
+      if constexpr (TT > 4) {
+        // Many row tiles: one at a time in the fewest registers (the other wave of the SIMD
+        // fills its waits), up to the tiles that have rows.
+        typename Mma::Operand wf[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          wf[i] = Mma::operand(read_codes(st + w_row(i) * kRowBytes, frag));
+        Codes xc = read_codes(xs, frag);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          if (t < live) {  // wave-uniform
+            const typename Mma::Operand xf = Mma::operand(xc);
+            if (t + 1 < TT) xc = read_codes(xs + (t + 1) * WT * 16 * kRowBytes, frag);
+            const float sat = sa[16 * WT * t];
+            f32x4_t part[NT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) part[i] = Mma::product(wf[i], xf);
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              const float sc = sat * scale_of(i);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) acc[i][t][x] = fmaf(part[i][x], sc, acc[i][t][x]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        continue;
+      }
       // Row tile t's products are issued with tile t + 1's LDS reads before them and tile
       // t - 1's FMAs behind them, so that neither waits; the weights are converted between
       // the first tile's products.
@@ -728,10 +763,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
       const auto add = [&](int t) {
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-          float sbt = sbv[kSwiglu && i >= NT / 2 ? 1 : 0];
-          if constexpr (!kSwiglu && C::kNBlocks > 1)
-            sbt = n_in_block + w_row(i) < kFp8Block ? sbv[0] : sbv[1];  // wave-uniform
-          const float sc = sat[t] * sbt;
+          const float sc = sat[t] * scale_of(i);
 #pragma unroll
           for (int x = 0; x < 4; ++x) acc[i][t][x] = fmaf(part[t & 1][i][x], sc, acc[i][t][x]);
         }
@@ -954,9 +986,10 @@ int run(const char *name, const GemmArgs &p, void *stream) {
 
 // The tiles a launch can take, narrowest first: weight rows x rows per tile.
 //   plain   128 x 32   128 x 64   256 x 128 (two-phase)   32 x 16, four slice groups
-//   SwiGLU  256 x 32   256 x 64   256 x 128 (two-phase)
-constexpr int kTileRowsOf[4] = {32, 64, 128, 16};
+//   SwiGLU  256 x 32   256 x 64   256 x 128 (two-phase)   256 x 192
+constexpr int kPlainRowsOf[4] = {32, 64, 128, 16};
 constexpr int kPlainWidthOf[4] = {128, 128, 256, 32};
+constexpr int kSwigluRowsOf[4] = {32, 64, 128, 192};
 
 struct Plan {
   int tile, ways;
@@ -966,13 +999,15 @@ struct Plan {
 // estimate in microseconds, from two measured rates. A CU takes in about 0.32 MB/us
 // (0.0031 us per LDS row of 128 bytes; 64 KB in flight and any tile shape end there), so a
 // step costs 0.0031 us x (weight rows + rows); the SwiGLU form's conversions and BF16 products
-// cost 0.0205 us per row and step (0.0151 in the two-phase loop), the FP8 products stay below
-// the loads. An item costs 2 us more (its first loads), 0.7 where two blocks fit a CU and one
+// cost 0.0205 us per row and step (0.0165 in the two larger tiles; the two-phase loop's rows
+// come in 64s), the FP8 products stay below the loads. An item costs 2 us more (its first loads), 0.7 where two blocks fit a CU and one
 // loads while the other starts. A split adds a launch (6 with its wait) and writes and reads
 // its sums, at 2.5 and 4 TB/s. HBM bounds all of it (the experts' weights at 6 TB/s); a tenth
 // of the estimate stands for what does not run beside that. Checked where tiles meet: 256
 // experts, gate/up width 2048 x K 6144, 8 rows each 1065 us with 32-row tiles and 1100 with
-// 64; 32 rows each 1485 and 1237; 128 rows each 2858 with 64-row tiles and 2490 with 128.
+// 64; 32 rows each 1485 and 1237; 128 rows each 2858, 2490 and 2120 with 64-, 128- and
+// 192-row tiles (most of those experts pass 128 rows by a few); one matrix of 4096 rows 279, 194
+// and 275.
 template <bool kSwiglu>
 Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, int cus) {
   const double used = experts > 0 ? static_cast<double>(experts < rows ? experts : rows) : 1.0;
@@ -981,8 +1016,8 @@ Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, i
   const double weights = used * static_cast<double>(n) * static_cast<double>(k) * (kSwiglu ? 2 : 1);
   Plan best = {0, 1};
   double best_us = 1e30;
-  for (int t = 0; t < (kSwiglu ? 3 : 4); ++t) {
-    const int bt = kTileRowsOf[t];
+  for (int t = 0; t < 4; ++t) {
+    const int bt = kSwiglu ? kSwigluRowsOf[t] : kPlainRowsOf[t];
     const int width = kSwiglu ? 2 * kFp8Block : kPlainWidthOf[t];
     const int bn_out = kSwiglu ? kFp8Block : width;
     // Row tiles per expert: exact for one matrix; for experts of `avg` rows on average, one
@@ -993,7 +1028,8 @@ Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, i
     const double live = experts > 0 ? avg / tiles : (avg < bt ? avg : bt);
     double step = 0.0031 * (width + live);
     if (kSwiglu) {
-      const double compute = (t == 2 ? 0.0151 : 0.0205) * live;
+      const double rows_done = t != 2 ? live : live > 64 ? 128 : 64;
+      const double compute = (t < 2 ? 0.0205 : 0.0165) * rows_done;
       if (compute > step) step = compute;
     }
     const double items = used * tiles * static_cast<double>((n + bn_out - 1) / bn_out);
@@ -1038,7 +1074,8 @@ int dispatch(const char *name, GemmArgs p, void *workspace, int64_t workspace_by
     switch (plan.tile) {
       case 0: rc = run<Cfg<2, 2, 8, 1, 1, 2>, true, kGrouped>(name, p, stream); break;
       case 1: rc = run<Cfg<4, 2, 4, 2, 1, 3>, true, kGrouped>(name, p, stream); break;
-      default: rc = run<Cfg<4, 4, 4, 2, 1, 3, true>, true, kGrouped>(name, p, stream); break;
+      case 2: rc = run<Cfg<4, 4, 4, 2, 1, 3, true>, true, kGrouped>(name, p, stream); break;
+      default: rc = run<Cfg<4, 6, 4, 2, 1, 2>, true, kGrouped>(name, p, stream); break;
     }
     if (rc != MOE_OK || plan.ways == 1) return rc;
     const int64_t groups = static_cast<int64_t>(p.rows) * ((p.n + kFp8Block - 1) / kFp8Block);

@@ -189,10 +189,12 @@ def _assert_quantised(codes, scale, ref, rel):
 
 # --------------------------------------------------------------------------------- dense
 
+# Each list reaches every tile the launcher picks among (the larger ones take thousands of rows).
 DENSE = [(1, 16, 16), (1, 6144, 2048), (2, 272, 6144), (5, 48, 144), (8, 2048, 656), (12, 128, 128),
          (13, 144, 512), (17, 272, 656), (33, 1360, 1040), (40, 128, 2048), (41, 384, 272),
          (70, 400, 1040), (129, 272, 256), (256, 1024, 528), (300, 2064, 400), (515, 256, 6144),
-         (1030, 1040, 144), (2100, 4112, 272)]
+         (1030, 1040, 144), (2100, 4112, 272), (3300, 1296, 400), (4700, 144, 400),
+         (1500, 2064, 784)]
 
 
 @pytest.mark.parametrize("m,n,k", DENSE)
@@ -207,7 +209,7 @@ def test_dense_exact_sums(hip, m, n, k):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 512, 2048), (9, 272, 656), (37, 400, 1040),
-                                   (300, 528, 2048), (600, 1024, 6144)])
+                                   (300, 528, 2048), (600, 1024, 6144), (3300, 1296, 400)])
 def test_dense_normal_operands(hip, m, n, k):
     rng = np.random.default_rng(m + n + k)
     a, sa = _normal_operand(rng, m, k, False)
@@ -258,7 +260,8 @@ def test_dense_nan_and_infinity_stay_in_their_row(hip):
 
 @pytest.mark.parametrize("m,n,k", [(1, 16, 16), (1, 2048, 6144), (7, 144, 272), (12, 256, 512),
                                    (30, 400, 1040), (64, 128, 656), (77, 1360, 1040),
-                                   (130, 272, 2048), (300, 528, 400)])
+                                   (130, 272, 2048), (300, 528, 400), (2900, 272, 400),
+                                   (4300, 400, 272), (3100, 1296, 400)])
 def test_dense_swiglu(hip, m, n, k):
     rng = np.random.default_rng(2 * m + n + k)
     a, sa = _normal_operand(rng, m, k, False)
@@ -375,7 +378,8 @@ GROUPED = [  # experts, rows, n, k, counts
     (1, 1, 16, 16, "even"), (4, 3, 272, 144, "even"), (9, 21, 272, 656, "skew"),
     (16, 130, 144, 512, "even"), (16, 513, 400, 272, "skew"), (64, 100, 256, 256, "skew"),
     (70, 2000, 128, 400, "skew"), (8, 700, 1040, 528, "even"), (130, 260, 160, 128, "even"),
-    (3, 1500, 272, 1040, "skew"), (2048, 300, 32, 48, "even"), (5, 1100, 528, 400, "even")]
+    (3, 1500, 272, 1040, "skew"), (2048, 300, 32, 48, "even"), (5, 1100, 528, 400, "even"),
+    (8, 4800, 144, 400, "skew"), (12, 3387, 1040, 400, "skew"), (12, 3600, 1040, 272, "even")]
 
 
 @pytest.mark.parametrize("experts,rows,n,k,kind", GROUPED)
@@ -439,7 +443,9 @@ def test_grouped_offsets_that_are_no_prefix_sum_stay_in_range(hip, off):
 GROUPED_SWIGLU = [  # experts, tokens, top_k, mi, k, counts
     (1, 1, 1, 16, 16, "even"), (8, 3, 2, 128, 272, "even"), (9, 33, 3, 272, 656, "skew"),
     (16, 65, 4, 144, 512, "even"), (16, 300, 4, 400, 272, "skew"), (64, 20, 8, 256, 256, "skew"),
-    (4, 500, 2, 272, 1040, "skew"), (6, 400, 3, 160, 400, "even"), (40, 900, 2, 144, 272, "skew")]
+    (4, 500, 2, 272, 1040, "skew"), (6, 400, 3, 160, 400, "even"), (40, 900, 2, 144, 272, "skew"),
+    (20, 1902, 2, 144, 400, "skew"), (20, 1630, 3, 400, 400, "skew"), (17, 2400, 1, 784, 400, "even"),
+    (5, 120, 2, 4112, 144, "skew"), (70, 4500, 2, 272, 272, "even")]
 
 
 @pytest.mark.parametrize("experts,tokens,top_k,mi,k,kind", GROUPED_SWIGLU)
