@@ -746,9 +746,11 @@ def _swiglu_workspace(ws, rows, num_experts, width, k, device, stream):
     need = load().moe_fp8_swiglu_workspace_bytes(rows, num_experts, width, k)
     if need == 0:
         return None, None, 0
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
+    if stream is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    else:  # from that stream's pool: what the block held before was ordered on it
+        with torch.cuda.stream(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
     return ws, _p(ws), need
 
 
@@ -1121,6 +1123,10 @@ class Fp8ExpertTable:
         self.gate_up = bool(gate_up)
         nb = 2 * _fp8_blocks(n // 2) if gate_up else _fp8_blocks(n)
         s_shape = (nb, _fp8_blocks(k))
+        if device is not None:
+            device = torch.device(device)
+            if device.index is None and device.type == "cuda":
+                device = torch.device("cuda", torch.cuda.current_device())
         wp, sp = [], []
         for e, (w, s) in enumerate(zip(weights, scales)):
             if (w is None) != (s is None):
@@ -1141,15 +1147,15 @@ class Fp8ExpertTable:
                 raise ValueError(f"expert {e}: weights must be 16-byte aligned")
             if device is None:
                 device = w.device
-            if w.device != s.device or w.device != torch.device(device):
+            if w.device != device or s.device != device:
                 raise ValueError(f"expert {e}: lies on another device")
             wp.append(w.data_ptr())
             sp.append(s.data_ptr())
         if device is None:  # every entry null
             device = torch.device("cuda", torch.cuda.current_device())
         self._keep = (list(weights), list(scales))
-        self.weight_ptrs = torch.tensor(wp, dtype=torch.int64, device=device)
-        self.scale_ptrs = torch.tensor(sp, dtype=torch.int64, device=device)
+        ptrs = torch.tensor([wp, sp], dtype=torch.int64, device=device)  # one transfer
+        self.weight_ptrs, self.scale_ptrs = ptrs[0], ptrs[1]
         self.present = [w is not None for w in weights]
 
 

@@ -116,7 +116,7 @@ struct Cfg {
   static_assert(BN / 8 % kSliceWaves == 0, "whole weight instructions per wave");
   static_assert(kXInstr % kSliceWaves == 0 || kXInstr < kSliceWaves, "row instructions");
   static_assert(kSliceWaves * 64 >= BT, "one scale instruction per wave covers the tile");
-  static_assert(BN % 64 == 0 || kFp8Block % BN == 0, "a tile's rows lie in kNBlocks blocks");
+  static_assert(BN % kFp8Block == 0 || kFp8Block % BN == 0, "scale blocks");
   // LDS: stages, a dump for loads that must not land anywhere, weight scales, tile prefix
   static constexpr int kDumpOff = ST * kStage;
   // Waves per SIMD the registers leave room for: as many as the LDS does, two blocks at most.
@@ -590,7 +590,6 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
     };
     // This wave's row tile t is tile t WT + wt; the tiles with rows are its first `live`.
     const int live = max((cnt + kR - 1) / kR - wt + WT - 1, 0) / WT;
-    const int n_in_block = n0 % kFp8Block;
 
     constexpr int kWaitN = C::kLoads * (ST - 2);
     static_assert(ST >= 2 && kWaitN < 64, "vmcnt holds 6 bits");
@@ -666,7 +665,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
             const int i = q & 1, t = q >> 1;
             float sbt = sbv[kSwiglu ? i : 0];
             if constexpr (!kSwiglu && C::kNBlocks > 1)
-              sbt = n_in_block + w_row(4 * i) < kFp8Block ? sbv[0] : sbv[1];
+              sbt = w_row(4 * i) < kFp8Block ? sbv[0] : sbv[1];
             const float sc = sat[t] * sbt;
 #pragma unroll
             for (int x = m * 16 / Wide::kParts; x < (m + 1) * 16 / Wide::kParts; ++x)
@@ -716,7 +715,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
       if (live == 0) continue;  // wave-uniform; the loop ends with no barrier of its own
       const auto scale_of = [&](int i) {
         if constexpr (!kSwiglu && C::kNBlocks > 1)
-          return n_in_block + w_row(i) < kFp8Block ? sbv[0] : sbv[1];  // wave-uniform
+          return w_row(i) < kFp8Block ? sbv[0] : sbv[1];  // wave-uniform
         else
           return sbv[kSwiglu && i >= NT / 2 ? 1 : 0];
       };
@@ -942,33 +941,51 @@ int compute_units(int device) {
   return cus[device];
 }
 
-// Raises the dynamic LDS limit of the kernel of configuration Key once per device.
-template <class Key>
-bool allow_lds(void (*kern)(GemmArgs), int device) {
+// The tiles a launch can take, narrowest first.
+template <bool kSwiglu>
+struct Tiles;
+template <>
+struct Tiles<false> {
+  using T0 = Cfg<2, 2, 4, 1, 1, 3>;        // 128 weight rows x 32 rows
+  using T1 = Cfg<4, 2, 2, 2, 1, 3>;        // 128 x 64
+  using T2 = Cfg<4, 4, 4, 2, 1, 3, true>;  // 256 x 128, two-phase
+  using T3 = Cfg<2, 1, 1, 1, 4, 3>;        // 32 x 16, four slice groups
+};
+template <>
+struct Tiles<true> {
+  using T0 = Cfg<2, 2, 8, 1, 1, 2>;        // 256 (gate and up) x 32
+  using T1 = Cfg<4, 2, 4, 2, 1, 3>;        // 256 x 64
+  using T2 = Cfg<4, 4, 4, 2, 1, 3, true>;  // 256 x 128, two-phase
+  using T3 = Cfg<4, 6, 4, 2, 1, 2>;        // 256 x 192
+};
+
+bool raise_lds(void (*kern)(GemmArgs)) {
+  return hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                             hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024) == hipSuccess;
+}
+
+// Raises the dynamic LDS limit of every kernel an entry point can launch, once per device: the
+// first call does it for all sizes.
+template <bool kSwiglu, bool kGrouped>
+bool allow_lds(int device) {
   static std::mutex mu;
   static bool done[kMaxDevices] = {};
   std::lock_guard<std::mutex> lock(mu);
   if (device >= 0 && device < kMaxDevices && done[device]) return true;
-  if (hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024) != hipSuccess)
+  using T = Tiles<kSwiglu>;
+  if (!raise_lds(fp8_gemm_kernel<typename T::T0, kSwiglu, kGrouped>) ||
+      !raise_lds(fp8_gemm_kernel<typename T::T1, kSwiglu, kGrouped>) ||
+      !raise_lds(fp8_gemm_kernel<typename T::T2, kSwiglu, kGrouped>) ||
+      !raise_lds(fp8_gemm_kernel<typename T::T3, kSwiglu, kGrouped>))
     return false;
   if (device >= 0 && device < kMaxDevices) done[device] = true;
   return true;
 }
 
-template <class C, bool kSwiglu, bool kGrouped>
-struct Key {};
-
 // A persistent launch of one configuration.
 template <class C, bool kSwiglu, bool kGrouped>
-int run(const char *name, const GemmArgs &p, void *stream) {
-  void (*const kern)(GemmArgs) = fp8_gemm_kernel<C, kSwiglu, kGrouped>;
-  const int device = current_device();
+int run(const char *name, const GemmArgs &p, int device, void *stream) {
   const int bytes = lds_bytes<C, kGrouped>(p);
-  if (!allow_lds<Key<C, kSwiglu, kGrouped>>(kern, device)) {
-    moe::set_error("%s: the device refuses %d bytes of LDS", name, bytes);
-    return MOE_ELAUNCH;
-  }
   const int bn_out = kSwiglu ? C::BN / 2 : C::BN;
   const int64_t n_tiles = (p.n + bn_out - 1) / bn_out;
   // Most row tiles there can be: every expert's last tile may be partial.
@@ -980,16 +997,9 @@ int run(const char *name, const GemmArgs &p, void *stream) {
   const int64_t resident = (per_cu < 1 ? 1 : per_cu) * compute_units(device);
   const int64_t items = row_tiles * n_tiles * p.ways;
   const int64_t grid = items < resident ? items : resident;
-  return moe::launch(name, kern, dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), bytes,
-                     stream, p);
+  return moe::launch(name, fp8_gemm_kernel<C, kSwiglu, kGrouped>,
+                     dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), bytes, stream, p);
 }
-
-// The tiles a launch can take, narrowest first: weight rows x rows per tile.
-//   plain   128 x 32   128 x 64   256 x 128 (two-phase)   32 x 16, four slice groups
-//   SwiGLU  256 x 32   256 x 64   256 x 128 (two-phase)   256 x 192
-constexpr int kPlainRowsOf[4] = {32, 64, 128, 16};
-constexpr int kPlainWidthOf[4] = {128, 128, 256, 32};
-constexpr int kSwigluRowsOf[4] = {32, 64, 128, 192};
 
 struct Plan {
   int tile, ways;
@@ -1017,9 +1027,10 @@ Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, i
   Plan best = {0, 1};
   double best_us = 1e30;
   for (int t = 0; t < 4; ++t) {
-    const int bt = kSwiglu ? kSwigluRowsOf[t] : kPlainRowsOf[t];
-    const int width = kSwiglu ? 2 * kFp8Block : kPlainWidthOf[t];
-    const int bn_out = kSwiglu ? kFp8Block : width;
+    using T = Tiles<kSwiglu>;
+    constexpr int kRows[4] = {T::T0::BT, T::T1::BT, T::T2::BT, T::T3::BT};
+    constexpr int kWidths[4] = {T::T0::BN, T::T1::BN, T::T2::BN, T::T3::BN};
+    const int bt = kRows[t], width = kWidths[t], bn_out = kSwiglu ? width / 2 : width;
     // Row tiles per expert: exact for one matrix; for experts of `avg` rows on average, one
     // where they seldom pass the tile, else half a tile more than the rows need.
     double tiles = experts > 0 ? (avg <= 0.75 * bt ? 1.0 : avg / bt + 0.5)
@@ -1059,38 +1070,33 @@ int64_t partial_bytes(const Plan &plan, int64_t rows, int64_t n) {
 template <bool kSwiglu, bool kGrouped>
 int dispatch(const char *name, GemmArgs p, void *workspace, int64_t workspace_bytes,
              void *stream) {
+  const int device = current_device();
+  MOE_REQUIRE_CODE((allow_lds<kSwiglu, kGrouped>(device)), MOE_ELAUNCH,
+                   "%s: the device refuses 160 KB of LDS to a block", name);
   const Plan plan = plan_for<kSwiglu>(p.rows, kGrouped ? p.num_experts : 0, p.n, p.k,
-                                      workspace != nullptr, compute_units(current_device()));
+                                      workspace != nullptr, compute_units(device));
   p.ways = plan.ways;
-  if constexpr (kSwiglu) {
-    if (plan.ways > 1) {
-      const int64_t need = partial_bytes(plan, p.rows, p.n);
-      MOE_REQUIRE_CODE(workspace_bytes >= need, MOE_ECAPACITY,
-                       "%s: a workspace of %lld bytes, these sizes need %lld", name,
-                       static_cast<long long>(workspace_bytes), static_cast<long long>(need));
-      p.partial = static_cast<float *>(workspace);
-    }
-    int rc;
-    switch (plan.tile) {
-      case 0: rc = run<Cfg<2, 2, 8, 1, 1, 2>, true, kGrouped>(name, p, stream); break;
-      case 1: rc = run<Cfg<4, 2, 4, 2, 1, 3>, true, kGrouped>(name, p, stream); break;
-      case 2: rc = run<Cfg<4, 4, 4, 2, 1, 3, true>, true, kGrouped>(name, p, stream); break;
-      default: rc = run<Cfg<4, 6, 4, 2, 1, 2>, true, kGrouped>(name, p, stream); break;
-    }
-    if (rc != MOE_OK || plan.ways == 1) return rc;
-    const int64_t groups = static_cast<int64_t>(p.rows) * ((p.n + kFp8Block - 1) / kFp8Block);
-    constexpr int kPer = kFinishThreads / 32;
-    return moe::launch(name, fp8_swiglu_finish_kernel<kGrouped>,
-                       dim3(static_cast<unsigned>((groups + kPer - 1) / kPer)),
-                       dim3(kFinishThreads), 0, stream, p);
-  } else {
-    switch (plan.tile) {
-      case 0: return run<Cfg<2, 2, 4, 1, 1, 3>, false, kGrouped>(name, p, stream);
-      case 1: return run<Cfg<4, 2, 2, 2, 1, 3>, false, kGrouped>(name, p, stream);
-      case 2: return run<Cfg<4, 4, 4, 2, 1, 3, true>, false, kGrouped>(name, p, stream);
-      default: return run<Cfg<2, 1, 1, 1, 4, 3>, false, kGrouped>(name, p, stream);
-    }
+  if (plan.ways > 1) {
+    const int64_t need = partial_bytes(plan, p.rows, p.n);
+    MOE_REQUIRE_CODE(workspace_bytes >= need, MOE_ECAPACITY,
+                     "%s: a workspace of %lld bytes, these sizes need %lld", name,
+                     static_cast<long long>(workspace_bytes), static_cast<long long>(need));
+    p.partial = static_cast<float *>(workspace);
   }
+  using T = Tiles<kSwiglu>;
+  int rc;
+  switch (plan.tile) {
+    case 0: rc = run<typename T::T0, kSwiglu, kGrouped>(name, p, device, stream); break;
+    case 1: rc = run<typename T::T1, kSwiglu, kGrouped>(name, p, device, stream); break;
+    case 2: rc = run<typename T::T2, kSwiglu, kGrouped>(name, p, device, stream); break;
+    default: rc = run<typename T::T3, kSwiglu, kGrouped>(name, p, device, stream); break;
+  }
+  if (rc != MOE_OK || plan.ways == 1) return rc;
+  const int64_t groups = static_cast<int64_t>(p.rows) * ((p.n + kFp8Block - 1) / kFp8Block);
+  constexpr int kPer = kFinishThreads / 32;
+  return moe::launch(name, fp8_swiglu_finish_kernel<kGrouped>,
+                     dim3(static_cast<unsigned>((groups + kPer - 1) / kPer)),
+                     dim3(kFinishThreads), 0, stream, p);
 }
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

@@ -582,7 +582,7 @@ int moe_w4a16_gemv_union_swiglu(const uint16_t *a, int64_t lda, int32_t a_rows,
  * multiple of 16 in [16, MOE_FP8_MAX_K]; lda and the weight's leading dimension at least k,
  * multiples of 16 and below 2^22; ld_a_scale >= ceil(k / 128) and below 2^20; code pointers
  * 16-byte and scale pointers 4-byte aligned; required pointers non-NULL when there are rows.
- * Every row count may be 0 (nothing is enqueued).
+ * Every row count may be 0 (nothing is enqueued) and is at most 2^30.
  */
 #define MOE_FP8_MAX_K 32768
 
@@ -601,7 +601,7 @@ int moe_w4a16_gemv_union_swiglu(const uint16_t *a, int64_t lda, int32_t a_rows,
  *   scale  float [rows, ld_scale]  out: ceil(cols / 128) per row
  * Requirements (else MOE_EINVAL): rows >= 0; cols >= 0 and cols % 16 == 0; ld_x >= cols, a
  * multiple of 8; ld_q >= cols, a multiple of 16; ld_scale >= ceil(cols / 128); x and q
- * 16-byte aligned, scale 4-byte aligned, non-NULL when rows * cols > 0; fewer than 2^28
+ * 16-byte aligned, scale 4-byte aligned, non-NULL when rows * cols > 0; fewer than 2^29
  * groups.
  */
 int moe_quant_fp8(const uint16_t *x, int64_t ld_x, uint8_t *q, int64_t ld_q, float *scale,

@@ -677,6 +677,28 @@ def test_layer_captured_and_replayed(hip):
         assert torch.equal(got, eager)
 
 
+def test_layer_with_a_bf16_shared_term_and_without_rows(hip):
+    """The shared term as a BF16 SharedExpert and as a tensor give the same bits; no rows
+    enqueue nothing."""
+    rows, experts, top_k, hidden, mi = 20, 6, 2, 256, 128
+    rng, _, _, _, (gt, dt), ws, _ = _layer(hip, 24, rows, experts, top_k, hidden, mi)
+    x, ids, w = _layer_inputs(rng, rows, experts, top_k, hidden)
+    x, ids, w = x.cuda(), _dev(ids), _dev(w)
+    g, u, d = (_bf16(rng.standard_normal(s) / 16).cuda() for s in ((64, hidden), (64, hidden),
+                                                                   (hidden, 64)))
+    sh = hip.SharedExpert(g, u, d, rows)
+    outs = [torch.empty((rows, hidden), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    hip.moe_layer_fp8(x, ids, w, gt, dt, 7.0, ws, outs[0], sh)
+    hip.moe_layer_fp8(x, ids, w, gt, dt, 7.0, ws, outs[1], sh(x, 7.0))
+    assert torch.equal(outs[0], outs[1])
+    hip.moe_layer_fp8(x[:0], ids[:0], w[:0], gt, dt, 7.0, ws, outs[1][:0])
+    with pytest.raises(ValueError):
+        hip.moe_layer_fp8(x, ids, w, gt, dt, 7.0, hip.Fp8Workspace(rows, 3, experts, hidden, mi),
+                          outs[0])
+    with pytest.raises(ValueError):
+        hip.moe_layer_fp8(x, ids, w, dt, gt, 7.0, ws, outs[0])
+
+
 def test_calls_run_on_the_given_stream(hip):
     """Two independent chains on two streams, each with its own buffers."""
     rng = np.random.default_rng(23)
