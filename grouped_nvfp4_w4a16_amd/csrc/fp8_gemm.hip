@@ -240,15 +240,16 @@ struct Item {
   int m0, cnt, n0, n_valid;
 };
 
-// The items of a launch with tiles of BT rows x kBnOut output columns. Grouped: `prefix`
-// (LDS, num_experts + 1) holds the row tiles before each expert, counted from the offsets.
+// The items of a launch with tiles of BT rows x kBnOut output columns (fewer than 2^31: the host
+// checks). Grouped: `prefix` (LDS, num_experts + 1) holds the row tiles before each expert,
+// counted from the offsets.
 template <int BT, int kBnOut, bool kGrouped>
 struct Items {
   // Every thread of the block calls it (it holds a barrier).
-  static __device__ __forceinline__ int64_t count(const GemmArgs &p, int *prefix, int lane,
-                                                  int wave) {
-    const int n_tiles = (p.n + kBnOut - 1) / kBnOut;
-    if constexpr (!kGrouped) return static_cast<int64_t>((p.rows + BT - 1) / BT) * n_tiles;
+  static __device__ __forceinline__ uint32_t count(const GemmArgs &p, int *prefix, int lane,
+                                                   int wave) {
+    const uint32_t n_tiles = (p.n + kBnOut - 1) / kBnOut;
+    if constexpr (!kGrouped) return (p.rows + BT - 1) / BT * n_tiles;
     if (wave == 0) {
       int carry = 0;
       for (int base = 0; base < p.num_experts; base += 64) {
@@ -270,16 +271,19 @@ struct Items {
       if (lane == 0) prefix[p.num_experts] = carry;
     }
     __syncthreads();
-    return static_cast<int64_t>(__builtin_amdgcn_readfirstlane(prefix[p.num_experts])) * n_tiles;
+    // At most the host's bound, also for offsets that are no prefix sum.
+    const uint32_t tiles = max(min(__builtin_amdgcn_readfirstlane(prefix[p.num_experts]),
+                                   p.rows / BT + min(p.num_experts, p.rows)), 0);
+    return tiles * n_tiles;
   }
 
   // Item number `item`; false for a number that offsets which are no prefix sum lead out of
   // the expert's rows (every access so stays in range).
   static __device__ __forceinline__ bool get(const GemmArgs &p, const int *prefix, int lane,
-                                             int64_t item, Item &it) {
-    const int n_tiles = (p.n + kBnOut - 1) / kBnOut;
-    int lo, hi;     // the expert's rows
-    int64_t local;  // the item's number within the expert
+                                             uint32_t item, Item &it) {
+    const uint32_t n_tiles = (p.n + kBnOut - 1) / kBnOut;
+    int lo, hi;      // the expert's rows
+    uint32_t local;  // the item's number within the expert
     if constexpr (kGrouped) {
       const int ty = static_cast<int>(item / n_tiles);
       // The last expert whose prefix is at most ty (prefixes do not decrease).
@@ -291,10 +295,11 @@ struct Items {
       const int e = __builtin_amdgcn_readfirstlane(max(below - 1, 0));
       lo = max(p.offsets[e], 0);
       hi = min(p.offsets[e + 1], p.rows);
-      local = item - static_cast<int64_t>(__builtin_amdgcn_readfirstlane(prefix[e])) * n_tiles;
+      const int before = __builtin_amdgcn_readfirstlane(prefix[e]);
       it.w0 = reinterpret_cast<const uint8_t *>(p.w_ptrs[e]);
       it.s0 = reinterpret_cast<const float *>(p.s_ptrs[e]);
-      if (it.w0 == nullptr || hi <= lo || local < 0) return false;
+      if (it.w0 == nullptr || hi <= lo || before < 0 || before > ty) return false;
+      local = item - static_cast<uint32_t>(before) * n_tiles;
       it.w1 = it.w0 + static_cast<int64_t>(p.n) * p.ldw;
       it.s1 = it.s0 + static_cast<int64_t>((p.n + kFp8Block - 1) / kFp8Block) *
                           ((p.k + kFp8Block - 1) / kFp8Block);
@@ -309,20 +314,21 @@ struct Items {
     }
     // Within an expert, kGroupM row tiles at a time, the row tile fastest: the items that run
     // at once share both weight tiles and row tiles.
-    const int m_tiles = (hi - lo + BT - 1) / BT;
-    const int64_t grp = local / (static_cast<int64_t>(kGroupM) * n_tiles);
-    const int g0 = static_cast<int>(grp) * kGroupM;
+    const uint32_t m_tiles = (hi - lo + BT - 1) / BT;
+    const uint32_t g0 = local / (kGroupM * n_tiles) * kGroupM;
     if (g0 >= m_tiles) return false;
-    const int g_rows = min(kGroupM, m_tiles - g0);
-    const int in_grp = static_cast<int>(local - grp * kGroupM * n_tiles);
-    it.n0 = in_grp / g_rows * kBnOut;
+    const uint32_t g_rows = min(static_cast<uint32_t>(kGroupM), m_tiles - g0);
+    const uint32_t in_grp = local - g0 * n_tiles;
+    const uint32_t col = in_grp / g_rows;
+    if (col >= n_tiles) return false;
+    it.n0 = static_cast<int>(col) * kBnOut;
     // The tiles of an expert hold equal numbers of rows (a multiple of 16): as many as BT allows
     // at least, none with a few leftover rows that would cost it all the expert's weights.
     const int per = kGrouped ? ((hi - lo + m_tiles - 1) / m_tiles + 15) / 16 * 16 : BT;
-    it.m0 = lo + (g0 + in_grp % g_rows) * per;
+    it.m0 = lo + static_cast<int>(g0 + in_grp - col * g_rows) * per;
     it.cnt = min(per, hi - it.m0);
     it.n_valid = min(kBnOut, p.n - it.n0);
-    return it.n0 < p.n && it.cnt > 0;
+    return it.cnt > 0;
   }
 };
 
@@ -330,15 +336,15 @@ struct Items {
 // takes a contiguous eighth, so that items with the same rows or weights run next to each
 // other on one L2.
 struct Share {
-  int64_t first, end;
-  int stride;
+  uint32_t first, end, stride;
 };
 
-__device__ __forceinline__ Share share_of(int64_t items) {
-  const int stride = gridDim.x;
-  if ((stride & 7) != 0) return {static_cast<int64_t>(blockIdx.x), items, stride};
-  const int xcd = blockIdx.x & 7;
-  return {items * xcd / 8 + (blockIdx.x >> 3), items * (xcd + 1) / 8, stride >> 3};
+__device__ __forceinline__ Share share_of(uint32_t items) {
+  const uint32_t blocks = gridDim.x, b = blockIdx.x;
+  if ((blocks & 7) != 0) return {b, items, blocks};
+  const uint64_t xcd = b & 7;
+  return {static_cast<uint32_t>(items * xcd >> 3) + (b >> 3),
+          static_cast<uint32_t>(items * (xcd + 1) >> 3), blocks >> 3};
 }
 
 // The item's rows as buffer resources: from the tile's first row, or (gathered) from row 0.
@@ -477,12 +483,12 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
   float *sb = reinterpret_cast<float *>(lds + C::kSbOff);  // [kNBlocks][kb_pad]
   int *prefix = reinterpret_cast<int *>(sb + C::kNBlocks * kb_pad);
   using Work = Items<BT, kBnOut, kGrouped>;
-  const int64_t tiles = Work::count(p, prefix, lane, wave);
+  const uint32_t tiles = Work::count(p, prefix, lane, wave);
   const int ways = kSwiglu ? p.ways : 1;
   const int split_kb = (kb_n + ways - 1) / ways;  // K blocks per split
   const Share mine = share_of(tiles * ways);
 
-  for (int64_t item = mine.first; item < mine.end; item += mine.stride) {
+  for (uint32_t item = mine.first; item < mine.end; item += mine.stride) {
     Item it;
     const int split = ways > 1 ? static_cast<int>(item / tiles) : 0;
     if (!Work::get(p, prefix, lane, item - split * tiles, it)) continue;
@@ -996,6 +1002,8 @@ int run(const char *name, const GemmArgs &p, int device, void *stream) {
   const int64_t per_cu = 160 * 1024 / bytes;
   const int64_t resident = (per_cu < 1 ? 1 : per_cu) * compute_units(device);
   const int64_t items = row_tiles * n_tiles * p.ways;
+  MOE_REQUIRE(items < (1ll << 31), "%s: too many tiles (%lld)", name,
+              static_cast<long long>(items));
   const int64_t grid = items < resident ? items : resident;
   return moe::launch(name, fp8_gemm_kernel<C, kSwiglu, kGrouped>,
                      dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), bytes, stream, p);
