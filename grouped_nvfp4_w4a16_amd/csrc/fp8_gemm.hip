@@ -9,25 +9,38 @@
 // One kernel template computes all four. The mathematics fixes its inner step: a block of
 // 128 k is exactly one v_mfma_f32_16x16x128_f8f6f4 (or four BF16 ones, below), whose FP32
 // result is multiplied by the block's two scales and added to the FP32 accumulator (4 FMAs
-// per lane and block product, issued under the next one). Weights are the MFMA's A operand and rows its B operand: a lane then
-// holds 4 consecutive outputs of ONE row, so its scale product is one number per 16-row tile
-// and weight block.
+// per lane and block product, issued under the next one). Weights are the MFMA's A operand and
+// rows its B operand: a lane then holds 4 consecutive outputs of ONE row, so its scale product
+// is one number per 16-row tile and weight block.
 //
 // Structure:
 //   - A block owns BN weight rows x BT rows over the whole K, in stages of KS slices of 128 k
-//     loaded straight into LDS (buffer_load ... lds), kStages - 1 stages ahead. LDS rows are
+//     loaded straight into LDS (buffer_load ... lds), ST - 1 stages ahead. LDS rows are
 //     128 bytes, 16-byte piece c of row r at c ^ (r & 7): the operand reads are conflict-free.
 //   - Waves: WN x WT over the tile, and KS groups that split the slices of a stage (the small
 //     tiles, whose sums are then joined in slice order).
 //   - Rows past the tile's valid ones, gather indices out of range and k past the end read
 //     zeros through their offset (past the buffer's end), without memory traffic.
-//   - Grouped form: blocks are persistent. Each counts the experts' row tiles from the
-//     offsets once (a prefix sum kept in LDS) and takes every gridDim-th (tile, weight tile)
-//     item: only experts with rows cost anything, however the rows are routed.
+//   - Blocks are persistent: an item is a row tile x a weight tile, each XCD takes a contiguous
+//     eighth of the items and its blocks take them in turn. Grouped form: a block counts the
+//     experts' row tiles from the offsets once (a prefix sum kept in LDS): only experts with
+//     rows cost anything, however the rows are routed.
 //   - SwiGLU form: the tile's weight rows are 128 gate rows and the same 128 up rows, a wave
 //     holding both sums of an output; one block so owns whole 128-column groups of the
 //     output and quantises them in its epilogue. Nothing is rounded between the FP32 sums and
-//     the codes.
+//     the codes. Few row tiles: K is split over blocks, which leave FP32 sums in the caller's
+//     workspace for a second launch (fp8_swiglu_finish_kernel).
+//
+// What bounds it and what it reaches (256 CUs, whole calls):
+//   - Many experts with few rows: HBM. 256 experts x 8 rows, N 6144 x K 2048: 534-557 us, 6.1
+//     of the 6.3 TB/s a plain read reaches; gate and up (2048 + 2048) x 6144: 1051 us, 6.1 TB/s.
+//   - Large products: what a CU takes in through LDS (0.32 MB/us from its L2), since every row
+//     of 128 codes is read by one tile in N / BN (M / BT): 4096 x 6144 x 2048 in 67 us, 1540
+//     TFLOP/s. The 256 x 128 tile reads 48.5 KB per step and CU for 8.4 MFLOP.
+//   - SwiGLU, experts of 128 rows: conversions to BF16 and BF16 products on the same SIMDs.
+//     32768 slots over 256 experts, (2048 + 2048) x 6144: 2120-2150 us, 770 TFLOP/s.
+//   - One token: the chain of a launch, the first loads and the steps of one tile, 5.7 us of
+//     kernel at 1 x 6144 x 2048.
 #include <mutex>
 #include <type_traits>
 
@@ -1018,14 +1031,31 @@ struct Plan {
 // (0.0031 us per LDS row of 128 bytes; 64 KB in flight and any tile shape end there), so a
 // step costs 0.0031 us x (weight rows + rows); the SwiGLU form's conversions and BF16 products
 // cost 0.0205 us per row and step (0.0165 in the two larger tiles; the two-phase loop's rows
-// come in 64s), the FP8 products stay below the loads. An item costs 2 us more (its first loads), 0.7 where two blocks fit a CU and one
-// loads while the other starts. A split adds a launch (6 with its wait) and writes and reads
-// its sums, at 2.5 and 4 TB/s. HBM bounds all of it (the experts' weights at 6 TB/s); a tenth
-// of the estimate stands for what does not run beside that. Checked where tiles meet: 256
-// experts, gate/up width 2048 x K 6144, 8 rows each 1065 us with 32-row tiles and 1100 with
-// 64; 32 rows each 1485 and 1237; 128 rows each 2858, 2490 and 2120 with 64-, 128- and
-// 192-row tiles (most of those experts pass 128 rows by a few); one matrix of 4096 rows 279, 194
-// and 275.
+// come in 64s), the FP8 products stay below the loads. An item costs 2 us more (its first
+// loads), 0.7 where two blocks fit a CU and one loads while the other starts, 1 where they
+// also join slice sums. A split adds a launch (6 with its wait) and writes and reads its sums,
+// at 2.5 and 4 TB/s. HBM bounds all of it (the experts' weights at 6 TB/s); a tenth of the
+// estimate stands for what does not run beside that.
+//
+// Both sides, measured in us, the one taken marked:
+//   plain, N 6144 x K 2048            32 x 16   128 x 32   128 x 64   256 x 128
+//     1 row                              9.3*       10.7        9.9        14.4
+//     64 rows                            9.1*        9.7       12.7        15.0
+//     256 rows                          25.6        13.1*      13.5        19.5
+//     1024 rows                         90.8        35.5       28.3        23.1*
+//     4096 rows                          348         128       95.3        72.0*
+//     256 experts, 8 rows each           691         557*       562         561
+//     256 experts, 32 rows each         1278         648        605*        607
+//     256 experts, 128 rows each        3985        1518       1227         896*
+//   SwiGLU, width 2048 x K 6144       256 x 32   256 x 64   256 x 128   256 x 192
+//     256 experts, 8 rows each          1065*       1100
+//     256 experts, 32 rows each         1485        1237*
+//     256 experts, 128 rows each                    2858        2490        2120*
+//     4096 rows                                      279         194*        275
+//   (most of those experts of 128 rows pass 128 by a few: they would take two 128-row tiles)
+//   split of K, the same width            1          2          4           8
+//     8 rows, 256 x 32                  38.9       23.8       16.5        14.0*
+//     192 rows, 256 x 64                66.5       41.7       30.6*       36.7
 template <bool kSwiglu>
 Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, int cus) {
   const double used = experts > 0 ? static_cast<double>(experts < rows ? experts : rows) : 1.0;
@@ -1056,9 +1086,8 @@ Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, i
       if (ways > 1 && (items * ways > 1.5 * cus || kb < 3 * ways)) break;
       double rounds = static_cast<double>(static_cast<int64_t>((items * ways + cus - 1) / cus));
       if (rounds < 1.0) rounds = 1.0;
-      const bool two_fit = kSwiglu ? t == 0 : t != 2;
-      double us = rounds * (static_cast<double>((kb + ways - 1) / ways) * step +
-                            (two_fit ? 0.7 : 2.0));
+      const double start = kSwiglu ? (t == 0 ? 0.7 : 2.0) : t < 2 ? 0.7 : t == 2 ? 2.0 : 1.0;
+      double us = rounds * (static_cast<double>((kb + ways - 1) / ways) * step + start);
       us = 0.1 * us + (us < weights / 6e6 ? weights / 6e6 : us);
       if (ways > 1)
         us += 6.0 + static_cast<double>(ways) * rows * n * 8.0 * (1.0 / 2.5e6 + 1.0 / 4e6);

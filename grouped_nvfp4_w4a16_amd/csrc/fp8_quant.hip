@@ -1,7 +1,8 @@
 // moe_quant_fp8: BF16 rows to E4M3 codes with one FP32 scale per (row, 128 columns), the
 // form the FP8 GEMMs take their rows in.
 //
-// Bound by memory: 2 bytes read and 1.03 written per value. 8 lanes share a group of 128
+// Bound by memory: 2 bytes read and 1.03 written per value: 4096 x 6144 in 13.0 us, 32768 rows
+// in 104 us (5.9 TB/s; a plain copy reaches 4.8, a plain read 6.3). 8 lanes share a group of 128
 // values, 16 values (two 16-byte loads, one 16-byte store) per lane, so a wave reads 2 KB and
 // writes 1 KB of consecutive columns. The magnitudes' maximum is taken on pairs of BF16
 // patterns at once (16-bit integer maxima). The quotients are the IEEE ones without a division
