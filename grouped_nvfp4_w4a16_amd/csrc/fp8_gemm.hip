@@ -38,7 +38,7 @@
 //     of 128 codes is read by one tile in N / BN (M / BT): 4096 x 6144 x 2048 in 67 us, 1540
 //     TFLOP/s. The 256 x 128 tile reads 48.5 KB per step and CU for 8.4 MFLOP.
 //   - SwiGLU, experts of 128 rows: conversions to BF16 and BF16 products on the same SIMDs.
-//     32768 slots over 256 experts, (2048 + 2048) x 6144: 2120-2150 us, 770 TFLOP/s.
+//     32768 slots over 256 experts, (2048 + 2048) x 6144: 2050 us, 800 TFLOP/s.
 //   - One token: the chain of a launch, the first loads and the steps of one tile, 5.7 us of
 //     kernel at 1 x 6144 x 2048.
 #include <mutex>
@@ -95,11 +95,11 @@ struct GemmArgs {
 };
 
 // One stage's loads of a wave: its K block, scalar offset, offset bits for what lies past K, and
-// its slice in LDS.
+// where its slice's weights and rows go in LDS.
 struct StageLoads {
   int kb, soff;
   uint32_t dead, s_dead;
-  uint8_t *st;
+  uint8_t *w, *x;
 };
 
 // Compile-time shape of a kernel: NT 16-row weight tiles and TT 16-row row tiles per wave,
@@ -117,8 +117,14 @@ struct Cfg {
   static constexpr int kWaves = kSliceWaves * KS, kThreads = 64 * kWaves;
   static constexpr int kScaleFloats = BT > 64 ? BT : 64;
   static constexpr int kWBytes = BN * kRowBytes, kXBytes = BT * kRowBytes;
-  static constexpr int kSlice = kWBytes + kXBytes + 4 * kScaleFloats;
+  static constexpr int kXSlice = kXBytes + 4 * kScaleFloats;
+  static constexpr int kSlice = kWBytes + kXSlice;
   static constexpr int kStage = KS * kSlice;
+  // Tall tiles hold ST stages of rows but only ST - 1 of weights: a wave keeps a step's weights
+  // in registers, so their buffer is free again early in the step.
+  static constexpr bool kTall = TT > 4;
+  static_assert(!kTall || (KS == 1 && ST == 3), "two weight buffers, three row buffers");
+  static constexpr int kStages = kTall ? 2 * kWBytes + 3 * kXSlice : ST * kStage;
   // 1 KB wave instructions per wave and stage
   static constexpr int kWLoads = BN / 8 / kSliceWaves;
   static constexpr int kXInstr = BT / 8;
@@ -131,9 +137,9 @@ struct Cfg {
   static_assert(kSliceWaves * 64 >= BT, "one scale instruction per wave covers the tile");
   static_assert(BN % kFp8Block == 0 || kFp8Block % BN == 0, "scale blocks");
   // LDS: stages, a dump for loads that must not land anywhere, weight scales, tile prefix
-  static constexpr int kDumpOff = ST * kStage;
+  static constexpr int kDumpOff = kStages;
   // Waves per SIMD the registers leave room for: as many as the LDS does, two blocks at most.
-  static constexpr int kMinWaves = kStage * ST <= 80 * 1024 - 6144 ? kWaves / 2 : kWaves / 4;
+  static constexpr int kMinWaves = kStages <= 80 * 1024 - 6144 ? kWaves / 2 : kWaves / 4;
   static constexpr int kSbOff = kDumpOff + 1024;
 };
 
@@ -541,10 +547,11 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
     // A stage's loads: kWLoads of weights, kXLoads of rows, one of row scales, issued singly
     // with piece(n): a wave's loads queue behind the other waves' (a CU takes in 1 KB in about
     // 28 cycles), so they are spread between the step's other work.
-    const auto stage_loads = [&](int j, int stage_off) {
+    const auto stage_loads_at = [&](int j, uint8_t *w, uint8_t *x) {
       StageLoads g;
       g.kb = kb0 + j * KS + slice;  // this wave's slice of the stage
-      g.st = lds + stage_off + slice * C::kSlice;
+      g.w = w;
+      g.x = x;
       // Bytes of this slice inside K; a piece past them is not loaded (zeros).
       const int left = g.kb < kb1 ? p.k - g.kb * kFp8Block : 0;
       g.dead = 16 * piece < left ? 0u : kNoLoad;
@@ -552,22 +559,26 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
       g.soff = left > 0 ? g.kb * kFp8Block : 0;
       return g;
     };
+    const auto stage_loads = [&](int j, int stage_off) {
+      uint8_t *st = lds + stage_off + slice * C::kSlice;
+      return stage_loads_at(j, st, st + C::kWBytes);
+    };
     const auto load_piece = [&](const StageLoads &g, int n) __attribute__((always_inline)) {
       if (n < C::kWLoads) {
         const int row = 8 * (sw * C::kWLoads + n);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            wr, (__attribute__((address_space(3))) void *)(g.st + row * kRowBytes), 16,
+            wr, (__attribute__((address_space(3))) void *)(g.w + row * kRowBytes), 16,
             static_cast<int>(w_voff[n < C::kWLoads ? n : 0] | g.dead), g.soff, 0, 0);
       } else if (n < C::kWLoads + C::kXLoads) {
         const int i = n - C::kWLoads, inst = sw * C::kXLoads + i;
-        uint8_t *dst = inst < C::kXInstr ? g.st + C::kWBytes + inst * 1024 : lds + C::kDumpOff;
+        uint8_t *dst = inst < C::kXInstr ? g.x + inst * 1024 : lds + C::kDumpOff;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rows.codes, (__attribute__((address_space(3))) void *)dst, 16,
             static_cast<int>(x_voff[i] | g.dead), g.soff, 0, 0);
       } else {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             rows.scales,
-            (__attribute__((address_space(3))) void *)(g.st + C::kWBytes + C::kXBytes +
+            (__attribute__((address_space(3))) void *)(g.x + C::kXBytes +
                                                        256 * (sw % (C::kScaleFloats / 64))),
             4, static_cast<int>(s_voff | g.s_dead), g.s_dead == 0 ? 4 * g.kb : 0, 0, 0);
       }
@@ -584,7 +595,13 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
     scales.load(p, it, kb_pad, tid);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < ST - 1; ++j) load_part(stage_loads(j, j * C::kStage), 0, 1, 1);
+    for (int j = 0; j < ST - 1; ++j) {
+      if constexpr (C::kTall)
+        load_part(stage_loads_at(j, lds + j * C::kWBytes, lds + 2 * C::kWBytes + j * C::kXSlice),
+                  0, 1, 1);
+      else
+        load_part(stage_loads(j, j * C::kStage), 0, 1, 1);
+    }
     scales.store(sb, kb_pad, tid);
     // Only the LDS stores are waited for here: the first step's barrier publishes them.
     __builtin_amdgcn_s_waitcnt(kLgkmWaitImm);
@@ -716,6 +733,72 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
       if (cnt > kR * WT) loop(std::integral_constant<int, 2>{});
       else loop(std::integral_constant<int, 1>{});
       if (group == 0) __builtin_amdgcn_s_barrier();
+    } else if constexpr (C::kTall) {
+      // Many row tiles: one at a time in the fewest registers (the other wave of the SIMD fills
+      // its waits), up to the tiles that have rows. Stage s + 2's rows are loaded when every
+      // wave has left step s - 1, its weights when every wave holds step s's in registers.
+      const int frag = r16 * kRowBytes + 16 * (g4 ^ (r16 & 7));
+      int w_cur = 0, x_cur = 0, x_fill = 2 * C::kXSlice;
+      const auto next_x = [](int off) { return off == 2 * C::kXSlice ? 0 : off + C::kXSlice; };
+      for (int s = 0; s < steps; ++s) {
+        __builtin_amdgcn_s_waitcnt(kWaitImm);  // this wave's loads of stage s are in LDS
+        __builtin_amdgcn_s_barrier();           // every wave's; and step s - 1's rows are read
+        uint8_t *ws = lds + w_cur;
+        const uint8_t *xs = lds + 2 * C::kWBytes + x_cur + wt * 16 * kRowBytes;
+        const StageLoads loads = stage_loads_at(s + 2, ws, lds + 2 * C::kWBytes + x_fill);
+        // Its loads, rows first, a quarter beside each of the first four tiles: all at once at
+        // the step's start they hold up every wave (32768 slots over 256 experts, gate and up
+        // 2048 wide, K 6144: 2257 us, 2050 this way, 2110 with two stages of both).
+        static_assert(TT >= 4 && C::kWLoads == C::kXLoads + 1, "half of the loads are weights'");
+        const auto issue = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+          for (int u = 0; u < C::kLoads; ++u)
+            if (u * 4 / C::kLoads == t) load_piece(loads, (u + C::kWLoads) % C::kLoads);
+        };
+        w_cur ^= C::kWBytes;
+        x_cur = next_x(x_cur);
+        x_fill = next_x(x_fill);
+        typename Mma::Operand wf[NT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          wf[i] = Mma::operand(read_codes(ws + w_row(i) * kRowBytes, frag));
+        Codes xc = read_codes(xs, frag);
+        const float *sa =
+            reinterpret_cast<const float *>(xs - wt * 16 * kRowBytes + C::kXBytes) + wt * 16 + r16;
+        const float sb0 = sb[kb0 + s], sb1 = sb[kb_pad + kb0 + s];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          if (t == 2) {  // before the weights' loads
+            __builtin_amdgcn_s_waitcnt(kLgkmWaitImm);
+            __builtin_amdgcn_s_barrier();  // every wave has read the step's weights
+          }
+          if (t < live) {  // wave-uniform
+            const typename Mma::Operand xf = Mma::operand(xc);
+            if (t + 1 < TT) xc = read_codes(xs + (t + 1) * WT * 16 * kRowBytes, frag);
+            const float sat = sa[16 * WT * t];
+            f32x4_t part[NT];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              if (i == NT / 2) {
+                __builtin_amdgcn_sched_barrier(0);
+                issue(t);
+                __builtin_amdgcn_sched_barrier(0);
+              }
+              part[i] = Mma::product(wf[i], xf);
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              const float sc = sat * (i >= NT / 2 ? sb1 : sb0);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) acc[i][t][x] = fmaf(part[i][x], sc, acc[i][t][x]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          } else {
+            issue(t);
+          }
+        }
+      }
     } else {
     const int frag = r16 * kRowBytes + 16 * (g4 ^ (r16 & 7));
     for (int s = 0; s < steps; ++s) {
@@ -738,35 +821,6 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
         else
           return sbv[kSwiglu && i >= NT / 2 ? 1 : 0];
       };
-      if constexpr (TT > 4) {
-        // Many row tiles: one at a time in the fewest registers (the other wave of the SIMD
-        // fills its waits), up to the tiles that have rows.
-        typename Mma::Operand wf[NT];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-          wf[i] = Mma::operand(read_codes(st + w_row(i) * kRowBytes, frag));
-        Codes xc = read_codes(xs, frag);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          if (t < live) {  // wave-uniform
-            const typename Mma::Operand xf = Mma::operand(xc);
-            if (t + 1 < TT) xc = read_codes(xs + (t + 1) * WT * 16 * kRowBytes, frag);
-            const float sat = sa[16 * WT * t];
-            f32x4_t part[NT];
-#pragma unroll
-            for (int i = 0; i < NT; ++i) part[i] = Mma::product(wf[i], xf);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              const float sc = sat * scale_of(i);
-#pragma unroll
-              for (int x = 0; x < 4; ++x) acc[i][t][x] = fmaf(part[i][x], sc, acc[i][t][x]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-          }
-        }
-        continue;
-      }
       // Row tile t's products are issued with tile t + 1's LDS reads before them and tile
       // t - 1's FMAs behind them, so that neither waits; the weights are converted between
       // the first tile's products.
@@ -975,7 +1029,7 @@ struct Tiles<true> {
   using T0 = Cfg<2, 2, 8, 1, 1, 2>;        // 256 (gate and up) x 32
   using T1 = Cfg<4, 2, 4, 2, 1, 3>;        // 256 x 64
   using T2 = Cfg<4, 4, 4, 2, 1, 3, true>;  // 256 x 128, two-phase
-  using T3 = Cfg<4, 6, 4, 2, 1, 2>;        // 256 x 192
+  using T3 = Cfg<4, 6, 4, 2, 1, 3>;        // 256 x 192, tall
 };
 
 bool raise_lds(void (*kern)(GemmArgs)) {
@@ -1050,7 +1104,7 @@ struct Plan {
 //   SwiGLU, width 2048 x K 6144       256 x 32   256 x 64   256 x 128   256 x 192
 //     256 experts, 8 rows each          1065*       1100
 //     256 experts, 32 rows each         1485        1237*
-//     256 experts, 128 rows each                    2858        2490        2120*
+//     256 experts, 128 rows each                    2858        2490        2050*
 //     4096 rows                                      279         194*        275
 //   (most of those experts of 128 rows pass 128 by a few: they would take two 128-row tiles)
 //   split of K, the same width            1          2          4           8
