@@ -24,6 +24,35 @@ __device__ __forceinline__ float fp8_scale(uint32_t amax_bits) {
   return s < 0x1p-126f ? 0x1p-126f : s;  // a select: NaN stays NaN
 }
 
+// Scales whose quotients need no division: nothing that matters to a code over- or underflows.
+__device__ __forceinline__ bool fp8_ordinary(float s) { return s >= 0x1p-64f && s <= 0x1p100f; }
+
+// v / s as IEEE rounds it, inv = 1 / s rounded, s ordinary: the first correction leaves the
+// product within an ulp, the second (its residual is exact) then rounds as the division does
+// (Markstein's theorem). A zero keeps v's sign. 6 operations, a division takes 11.
+__device__ __forceinline__ float fp8_quotient(float v, float s, float inv) {
+  float y = v * inv;
+  y = fmaf(fmaf(-y, s, v), inv, y);
+  y = fmaf(fmaf(-y, s, v), inv, y);
+  return __builtin_copysignf(y, v);
+}
+
+// silu(min(g, L)) * clamp(u, -L, L) in FP32 with moe::swiglu_clamp1's properties (selects keep a
+// NaN; e = e^-|g|, so nothing overflows; full range) in 20 operations instead of 50, for
+// outputs quantised to 4 significant bits. The hardware exponential ends at the normal numbers:
+// below g = -87 it takes e 2^64. Its argument's rounding moves e by |g| 2^-24, as the rounding
+// of the sum g itself does; the reciprocal is off by an ulp.
+__device__ __forceinline__ float fp8_swiglu(float g, float u, float limit) {
+  const float gc = g > limit ? limit : g;
+  const float uc = u > limit ? limit : (u < -limit ? -limit : u);
+  const float t = -1.44269504f * fabsf(gc);  // log2(e)
+  const bool tiny = t < -125.0f;
+  float e = __builtin_amdgcn_exp2f(tiny ? t + 64.0f : t);
+  e = tiny ? e * 0x1p-64f : e;
+  const float num = gc >= 0.0f ? gc : gc * e;
+  return num * __builtin_amdgcn_rcpf(1.0f + e) * uc;
+}
+
 // The codes of four quotients as four bytes, the first lowest.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);

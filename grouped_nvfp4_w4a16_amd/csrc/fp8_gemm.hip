@@ -48,7 +48,6 @@
 #include "common.h"
 #include "fp8.h"
 #include "nvfp4_decode.h"  // moe::pack_bf16x2
-#include "swiglu.h"
 
 namespace {
 
@@ -136,7 +135,7 @@ struct Cfg {
   static_assert(kXInstr % kSliceWaves == 0 || kXInstr < kSliceWaves, "row instructions");
   static_assert(kSliceWaves * 64 >= BT, "one scale instruction per wave covers the tile");
   static_assert(BN % kFp8Block == 0 || kFp8Block % BN == 0, "scale blocks");
-  // LDS: stages, a dump for loads that must not land anywhere, weight scales, tile prefix
+  // LDS: stages, a dump for loads that must not land anywhere, weight scales, item table
   static constexpr int kDumpOff = kStages;
   // Waves per SIMD the registers leave room for: as many as the LDS does, two blocks at most.
   static constexpr int kMinWaves = kStages <= 80 * 1024 - 6144 ? kWaves / 2 : kWaves / 4;
@@ -260,65 +259,111 @@ struct Item {
 };
 
 // The items of a launch with tiles of BT rows x kBnOut output columns (fewer than 2^31: the host
-// checks). Grouped: `prefix` (LDS, num_experts + 1) holds the row tiles before each expert,
-// counted from the offsets.
-template <int BT, int kBnOut, bool kGrouped>
+// checks). Grouped: the experts stand in order of their tiles' rows, the largest first (in
+// steps of 16 rows, the classes), so that the blocks' last items are the small ones. LDS words:
+// `table` holds the row tiles of each of the kClasses classes' predecessors, then their number,
+// and from kTable on per expert its class (4 bits) and the row tiles of its class before it.
+template <int BT, int kBnOut, bool kGrouped, int kWaves>
 struct Items {
-  // Every thread of the block calls it (it holds a barrier).
-  static __device__ __forceinline__ uint32_t count(const GemmArgs &p, int *prefix, int lane,
-                                                   int wave) {
+  static constexpr int kClasses = BT / 16;
+  static constexpr int kTable = 16, kPosBits = 28;  // row tiles fit: rows <= 2^30, BT >= 16
+  static constexpr uint32_t kPosMask = (1u << kPosBits) - 1, kNone = 15;  // class of no rows
+  static_assert(kClasses < 15, "a class fits 4 bits, the bases and the total 16 words");
+
+  // Rows of an expert's tiles: equal numbers (a multiple of 16), as many as BT allows at least,
+  // none with a few leftover rows that would cost it all the expert's weights.
+  static __device__ __forceinline__ int rows_per_tile(int rows, int m_tiles) {
+    return ((rows + m_tiles - 1) / m_tiles + 15) / 16 * 16;
+  }
+
+  // Every thread of the block calls it (it holds barriers).
+  static __device__ __forceinline__ uint32_t count(const GemmArgs &p, uint32_t *table, int tid) {
     const uint32_t n_tiles = (p.n + kBnOut - 1) / kBnOut;
     if constexpr (!kGrouped) return (p.rows + BT - 1) / BT * n_tiles;
-    if (wave == 0) {
-      int carry = 0;
+    uint32_t *experts = table + kTable;
+    for (int e = tid; e < p.num_experts; e += 64 * kWaves) {
+      const int cnt = min(p.offsets[e + 1], p.rows) - max(p.offsets[e], 0);
+      uint32_t word = kNone << kPosBits;
+      if (cnt > 0 && p.w_ptrs[e] != 0) {  // none where the expert is absent
+        const int t = (cnt + BT - 1) / BT;
+        word = static_cast<uint32_t>(kClasses - rows_per_tile(cnt, t) / 16) << kPosBits | t;
+      }
+      experts[e] = word;
+    }
+    __syncthreads();
+    const int lane = tid & 63;
+    for (int c = __builtin_amdgcn_readfirstlane(tid >> 6); c < kClasses; c += kWaves) {
+      uint32_t carry = 0;
       for (int base = 0; base < p.num_experts; base += 64) {
         const int e = base + lane;
-        int t = 0;
-        if (e < p.num_experts && p.w_ptrs[e] != 0) {  // none where the expert is absent
-          const int cnt = min(p.offsets[e + 1], p.rows) - max(p.offsets[e], 0);
-          t = cnt > 0 ? (cnt + BT - 1) / BT : 0;
-        }
-        int incl = t;
+        const uint32_t word = e < p.num_experts ? experts[e] : kNone << kPosBits;
+        const bool in = word >> kPosBits == static_cast<uint32_t>(c);
+        if (__ballot(in) == 0) continue;
+        const uint32_t t = in ? word & kPosMask : 0;
+        uint32_t incl = t;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-          const int u = __shfl_up(incl, d, 64);
+          const uint32_t u = __shfl_up(incl, d, 64);
           if (lane >= d) incl += u;
         }
-        if (e < p.num_experts) prefix[e] = carry + incl - t;
+        // Other waves look at the class alone, which stays. (The mask is for offsets that are
+        // no prefix sum.)
+        if (in) experts[e] = (word & ~kPosMask) | ((carry + incl - t) & kPosMask);
         carry += __shfl(incl, 63, 64);
       }
-      if (lane == 0) prefix[p.num_experts] = carry;
+      if (lane == 0) table[c] = carry;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t sum = 0;
+#pragma unroll
+      for (int c = 0; c < kClasses; ++c) {
+        const uint32_t t = table[c];
+        table[c] = sum;
+        sum += t;
+      }
+      table[kClasses] = sum;
     }
     __syncthreads();
     // At most the host's bound, also for offsets that are no prefix sum.
-    const uint32_t tiles = max(min(__builtin_amdgcn_readfirstlane(prefix[p.num_experts]),
-                                   p.rows / BT + min(p.num_experts, p.rows)), 0);
+    const uint32_t tiles =
+        min(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(table[kClasses])),
+            static_cast<uint32_t>(p.rows / BT + min(p.num_experts, p.rows)));
     return tiles * n_tiles;
   }
 
   // Item number `item`; false for a number that offsets which are no prefix sum lead out of
   // the expert's rows (every access so stays in range).
-  static __device__ __forceinline__ bool get(const GemmArgs &p, const int *prefix, int lane,
+  static __device__ __forceinline__ bool get(const GemmArgs &p, const uint32_t *table, int lane,
                                              uint32_t item, Item &it) {
     const uint32_t n_tiles = (p.n + kBnOut - 1) / kBnOut;
     int lo, hi;      // the expert's rows
     uint32_t local;  // the item's number within the expert
     if constexpr (kGrouped) {
-      const int ty = static_cast<int>(item / n_tiles);
-      // The last expert whose prefix is at most ty (prefixes do not decrease).
-      int below = 0;
+      const uint32_t tile = item / n_tiles;
+      // The last class that starts at most at the tile (an empty one starts with the next) ...
+      const uint32_t at_most = static_cast<uint32_t>(
+          __ballot(lane < kClasses && table[lane & 15] <= tile));
+      const int c = 31 - __clz(at_most | 1);
+      const uint32_t start = __builtin_amdgcn_readfirstlane(table[c]);
+      // ... and its last expert that does.
+      int e = -1;
       for (int base = 0; base < p.num_experts; base += 64) {
-        const int e = base + lane;
-        below += __popcll(__ballot(e < p.num_experts && prefix[e] <= ty));
+        const uint32_t word =
+            base + lane < p.num_experts ? table[kTable + base + lane] : kNone << kPosBits;
+        const uint64_t found = __ballot(word >> kPosBits == static_cast<uint32_t>(c) &&
+                                        (word & kPosMask) <= tile - start);
+        if (found != 0) e = base + 63 - __clzll(found);
       }
-      const int e = __builtin_amdgcn_readfirstlane(max(below - 1, 0));
+      if (e < 0) return false;
+      const uint32_t before =
+          start + (__builtin_amdgcn_readfirstlane(table[kTable + e]) & kPosMask);
       lo = max(p.offsets[e], 0);
       hi = min(p.offsets[e + 1], p.rows);
-      const int before = __builtin_amdgcn_readfirstlane(prefix[e]);
       it.w0 = reinterpret_cast<const uint8_t *>(p.w_ptrs[e]);
       it.s0 = reinterpret_cast<const float *>(p.s_ptrs[e]);
-      if (it.w0 == nullptr || hi <= lo || before < 0 || before > ty) return false;
-      local = item - static_cast<uint32_t>(before) * n_tiles;
+      if (it.w0 == nullptr || hi <= lo || before > tile) return false;
+      local = item - before * n_tiles;
       it.w1 = it.w0 + static_cast<int64_t>(p.n) * p.ldw;
       it.s1 = it.s0 + static_cast<int64_t>((p.n + kFp8Block - 1) / kFp8Block) *
                           ((p.k + kFp8Block - 1) / kFp8Block);
@@ -341,9 +386,7 @@ struct Items {
     const uint32_t col = in_grp / g_rows;
     if (col >= n_tiles) return false;
     it.n0 = static_cast<int>(col) * kBnOut;
-    // The tiles of an expert hold equal numbers of rows (a multiple of 16): as many as BT allows
-    // at least, none with a few leftover rows that would cost it all the expert's weights.
-    const int per = kGrouped ? ((hi - lo + m_tiles - 1) / m_tiles + 15) / 16 * 16 : BT;
+    const int per = kGrouped ? rows_per_tile(hi - lo, m_tiles) : BT;
     it.m0 = lo + static_cast<int>(g0 + in_grp - col * g_rows) * per;
     it.cnt = min(per, hi - it.m0);
     it.n_valid = min(kBnOut, p.n - it.n0);
@@ -351,20 +394,36 @@ struct Items {
   }
 };
 
-// This block's share of the items: workgroups go to the 8 XCDs round-robin, and each XCD
-// takes a contiguous eighth, so that items with the same rows or weights run next to each
-// other on one L2.
+// This block's items. Workgroups go to the 8 XCDs round-robin; items that are next to each
+// other share rows or weights and so run on one XCD's L2.
+// Dense: every XCD takes a contiguous eighth of the items, its blocks one after the other.
+// Grouped (items of falling size): every round of gridDim items goes to the XCDs in contiguous
+// eighths, the odd rounds backwards, so that a block's large items come with small ones
+// (8008 slots, Zipf, over 64 experts, gate and up 768 x 2048: 113 -> 102 us).
+template <bool kGrouped>
 struct Share {
-  uint32_t first, end, stride;
-};
+  uint32_t pos, items, stride;
 
-__device__ __forceinline__ Share share_of(uint32_t items) {
-  const uint32_t blocks = gridDim.x, b = blockIdx.x;
-  if ((blocks & 7) != 0) return {b, items, blocks};
-  const uint64_t xcd = b & 7;
-  return {static_cast<uint32_t>(items * xcd >> 3) + (b >> 3),
-          static_cast<uint32_t>(items * (xcd + 1) >> 3), blocks >> 3};
-}
+  __device__ __forceinline__ explicit Share(uint32_t n) {
+    const uint32_t blocks = gridDim.x, b = blockIdx.x;
+    const uint32_t xcd = b & 7, in_xcd = b >> 3;
+    const bool even = (blocks & 7) == 0;
+    items = n;
+    stride = blocks;
+    pos = even ? xcd * (blocks >> 3) + in_xcd : b;
+    if (!kGrouped && even) {
+      stride = blocks >> 3;
+      pos = static_cast<uint32_t>(static_cast<uint64_t>(n) * xcd >> 3) + in_xcd;
+      items = static_cast<uint32_t>(static_cast<uint64_t>(n) * (xcd + 1) >> 3);
+    }
+  }
+
+  // The block's item of a round; the rounds end with the first whose item is past the end.
+  __device__ __forceinline__ uint32_t item(uint32_t round) const {
+    const uint32_t at = kGrouped && (round & 1) != 0 ? stride - 1 - pos : pos;
+    return round * stride + at;
+  }
+};
 
 // The item's rows as buffer resources: from the tile's first row, or (gathered) from row 0.
 struct Rows {
@@ -420,25 +479,27 @@ struct WeightScales {
 
 // The SwiGLU form's epilogue. acc[i][t][x] is gate column col(i) + 4 gl + x of tile row
 // kR row(t) + rl (rl = lane % kR, gl = lane / kR), acc[i + NT / 2][t][x] the same column's up
-// sum; WN waves hold the 128 columns of a row. `lds` is free for BT rows of codes and (WN + 1) BT floats.
+// sum; WN waves hold the 128 columns of a row; the wave's first `live` row tiles have rows (the
+// epilogue of 192 rows takes 5 us). `lds` is free for BT rows of codes and (WN + 1) BT floats.
 constexpr int kCodeRow = kFp8Block + 16;  // staged code row, padded
 constexpr int swiglu_epilogue_bytes(int bt, int wn) { return bt * kCodeRow + 4 * wn * bt; }
 
 template <int NT, int TT, int kR, int WN, int BT, int kThreads, class Col, class Row>
 __device__ __forceinline__ void swiglu_epilogue(const GemmArgs &p, const Item &it, uint8_t *lds,
                                                 f32x4_t (&acc)[NT][TT], Col col, Row row,
-                                                int wn, int tid) {
+                                                int live, int wn, int tid) {
   constexpr int kH = NT / 2;
   const int lane = tid & 63, rl = lane % kR, gl = lane / kR;
   uint32_t *red = reinterpret_cast<uint32_t *>(lds + BT * kCodeRow);  // [WN][BT] magnitudes
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
+    if (t >= live) continue;  // wave-uniform
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < kH; ++i)
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const float v = moe::swiglu_clamp1(acc[i][t][x], acc[i + kH][t][x], p.limit);
+        const float v = moe::fp8_swiglu(acc[i][t][x], acc[i + kH][t][x], p.limit);
         acc[i][t][x] = v;
         // the width is a multiple of 16: a tile of 8 or 16 columns lies inside it or past it
         if (col(i) < it.n_valid) m = max(m, __float_as_uint(v) & 0x7FFFFFFFu);
@@ -451,6 +512,7 @@ __device__ __forceinline__ void swiglu_epilogue(const GemmArgs &p, const Item &i
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
+    if (t >= live) continue;
     const int r = kR * row(t) + rl;
     uint32_t m = 0;
 #pragma unroll
@@ -458,10 +520,21 @@ __device__ __forceinline__ void swiglu_epilogue(const GemmArgs &p, const Item &i
     const float s = moe::fp8_scale(m);
     if (wn == 0 && gl == 0 && r < it.cnt)
       p.q_scale[static_cast<int64_t>(it.m0 + r) * p.ld_qs + it.n0 / kFp8Block] = s;
+    const float inv = 1.0f / s;
+    const bool ordinary = moe::fp8_ordinary(s);
 #pragma unroll
-    for (int i = 0; i < kH; ++i)
+    for (int i = 0; i < kH; ++i) {
+      float q[4];
+      if (ordinary) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) q[x] = moe::fp8_quotient(acc[i][t][x], s, inv);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) q[x] = acc[i][t][x] / s;
+      }
       *reinterpret_cast<uint32_t *>(lds + r * kCodeRow + col(i) + 4 * gl) =
-          moe::e4m3x4(acc[i][t][0] / s, acc[i][t][1] / s, acc[i][t][2] / s, acc[i][t][3] / s);
+          moe::e4m3x4(q[0], q[1], q[2], q[3]);
+    }
   }
   __syncthreads();
   for (int u = tid; u < BT * (kFp8Block / 16); u += kThreads) {
@@ -477,7 +550,7 @@ template <class C, bool kGrouped>
 int lds_bytes(const GemmArgs &p) {
   const int kb = (p.k + kFp8Block - 1) / kFp8Block;
   const int kb_pad = (kb + C::KS - 1) / C::KS * C::KS;
-  return C::kSbOff + 4 * C::kNBlocks * kb_pad + (kGrouped ? 4 * (p.num_experts + 1) : 0);
+  return C::kSbOff + 4 * C::kNBlocks * kb_pad + (kGrouped ? 4 * (p.num_experts + 16) : 0);
 }
 
 template <class C, bool kSwiglu, bool kGrouped>
@@ -500,17 +573,19 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
   const int kb_n = (p.k + kFp8Block - 1) / kFp8Block;
   const int kb_pad = (kb_n + KS - 1) / KS * KS;
   float *sb = reinterpret_cast<float *>(lds + C::kSbOff);  // [kNBlocks][kb_pad]
-  int *prefix = reinterpret_cast<int *>(sb + C::kNBlocks * kb_pad);
-  using Work = Items<BT, kBnOut, kGrouped>;
-  const uint32_t tiles = Work::count(p, prefix, lane, wave);
+  uint32_t *table = reinterpret_cast<uint32_t *>(sb + C::kNBlocks * kb_pad);
+  using Work = Items<BT, kBnOut, kGrouped, C::kWaves>;
+  const uint32_t tiles = Work::count(p, table, tid);
   const int ways = kSwiglu ? p.ways : 1;
   const int split_kb = (kb_n + ways - 1) / ways;  // K blocks per split
-  const Share mine = share_of(tiles * ways);
+  const Share<kGrouped> mine(tiles * ways);
 
-  for (uint32_t item = mine.first; item < mine.end; item += mine.stride) {
+  for (uint32_t round = 0;; ++round) {
+    const uint32_t item = mine.item(round);
+    if (item >= mine.items) break;
     Item it;
     const int split = ways > 1 ? static_cast<int>(item / tiles) : 0;
-    if (!Work::get(p, prefix, lane, item - split * tiles, it)) continue;
+    if (!Work::get(p, table, lane, item - split * tiles, it)) continue;
     const int kb0 = split * split_kb, kb1 = min(kb_n, kb0 + split_kb);  // this item's K blocks
     const int steps = max(kb1 - kb0 + KS - 1, 0) / KS;
     const int n0 = it.n0, n_valid = it.n_valid, m0 = it.m0, cnt = it.cnt;
@@ -888,7 +963,7 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void fp8_gemm_kernel(Gem
         }
       } else {
         swiglu_epilogue<kAN, kAT, kR, WN, BT, C::kThreads>(
-            p, it, lds, acc, w_row, [&](int t) { return t * WT + wt; }, wn, tid);
+            p, it, lds, acc, w_row, [&](int t) { return t * WT + wt; }, live, wn, tid);
       }
     } else if constexpr (KS > 1) {
       // The slice groups' sums, joined in slice order.
@@ -974,7 +1049,7 @@ __global__ __launch_bounds__(kFinishThreads) void fp8_swiglu_finish_kernel(GemmA
       u += *reinterpret_cast<const f32x4_t *>(src + w * way + p.n);
     }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) v[x] = moe::swiglu_clamp1(g[x], u[x], p.limit);
+    for (int x = 0; x < 4; ++x) v[x] = moe::fp8_swiglu(g[x], u[x], p.limit);
   }
   uint32_t m = 0;
 #pragma unroll

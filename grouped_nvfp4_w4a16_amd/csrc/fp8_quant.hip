@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kThreads) void quant_kernel(
     f[2 * i] = __uint_as_float(w[i] << 16);
     f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  if (s >= 0x1p-100f && s <= 0x1p100f) {
+  if (moe::fp8_ordinary(s)) {
     const float inv = 1.0f / s;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {

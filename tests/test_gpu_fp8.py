@@ -336,6 +336,36 @@ def test_dense_swiglu_split_on_another_stream(hip):
         assert torch.equal(outs[0][1], outs[1][1])
 
 
+@pytest.mark.parametrize("k", [16, 2064])
+def test_dense_swiglu_far_negative_gates(hip, k):
+    """silu down to where e^g leaves the FP32 numbers, lifted by large up values. The gates are
+    exact. e^-|g| is off by |g| times the rounding of the exponent (2^-24, its 64 added 2^-24,
+    the constant 2^-26), by an ulp of the exponential and half a subnormal step; the
+    reciprocal by an ulp, the sum, three products and the scale's division by 2^-24 each."""
+    gates = np.array([1, 20, 60, 80, 86.5, 87.25, 88, 90, 95, 100, 103, 104, 120, 1000], np.float32)
+    m, n = len(gates), 144
+    a = np.zeros((m, k), np.uint8)
+    a[:, 0] = 0x38  # 1.0
+    sa = np.ones((m, fp8.blocks(k)), np.float32)
+    sa[:, 0] = gates
+    gate, up = np.zeros((n, k), np.uint8), np.zeros((n, k), np.uint8)
+    gate[:, 0], up[:, 0] = 0xB8, 0x38
+    one = np.ones((fp8.blocks(n), fp8.blocks(k)), np.float32)
+    q = torch.empty((m, n), dtype=torch.float8_e4m3fn, device="cuda")
+    s = torch.empty((m, fp8.blocks(n)), device="cuda")
+    hip.moe_dense_gate_up_swiglu_fp8(_f8(a), _dev(sa), _f8(gate), _dev(one), _f8(up),
+                                     _dev(one * np.float32(2.0 ** 100)), q, s, 3e38)
+    g = gates.astype(np.float64)
+    u = g * 2.0 ** 100
+    v = g * np.exp(-g) / (1 + np.exp(-g)) * u
+    bound = v * (2.25 * g + 10) * 2.0 ** -24 + (g + 1) * 2.0 ** -150 * u
+    got = s.cpu().numpy().astype(np.float64)
+    assert np.all(np.abs(got - (v / 448)[:, None]) <= (bound / 448 + 2.0 ** -126)[:, None])
+    codes = _host8(q)
+    assert np.all(codes[g <= 100] == 0xFE)  # -448, the group's largest
+    assert np.all(codes[g >= 110] & 0x7F == 0)
+
+
 def _swiglu_rel(a, sa, gate, up, ref, limit):
     """The largest error of v = silu(G) U in FP32, relative to its group's largest |v|: the
     sums' errors times the partial derivatives (|silu'| <= 1.1, |U| <= limit, |silu(G)| <=
@@ -438,6 +468,30 @@ def test_grouped_offsets_that_are_no_prefix_sum_stay_in_range(hip, off):
     hip.moe_w8a8_grouped_gemm(_f8(a), _dev(sa), table, _dev(np.array(off, np.int32)), c)
     torch.cuda.synchronize()
     assert _rest_is(buf, POISON16, rows, n)
+
+
+@pytest.mark.parametrize("experts,n", [(300, 144), (2048, 16), (70, 2064)])
+def test_grouped_experts_of_every_size(hip, experts, n):
+    """Counts from none to several tiles in no order, some experts absent: the work goes by size."""
+    rng = np.random.default_rng(experts)
+    k = 144
+    counts = np.where(rng.random(experts) < 0.3, 0, np.exp(rng.uniform(0, 4.5, experts)))
+    counts = counts.astype(np.int64)
+    counts[experts // 3] = 700
+    off = _offsets(counts)
+    rows = int(off[-1])
+    a, sa = _int_operand(rng, rows, k, False)
+    pool = [_int_operand(rng, n, k, True) for _ in range(7)]
+    weights = [None if e % 11 == 5 else pool[e % 7] for e in range(experts)]
+    buf, c = _out16(rows, n)
+    hip.moe_w8a8_grouped_gemm(_f8(a), _dev(sa), _table(hip, weights, n, k), _dev(off), c)
+    got, written = _bf16_f64(c), np.zeros(rows, bool)
+    for e, lo, hi in fp8.segments(off, rows):
+        if weights[e] is not None:
+            written[lo:hi] = True
+            want = codecs.round_bf16(fp8.product(a[lo:hi], sa[lo:hi], *weights[e]))
+            assert np.array_equal(got[lo:hi], want), e
+    assert _rest_is(buf, POISON16, rows, n, written)
 
 
 GROUPED_SWIGLU = [  # experts, tokens, top_k, mi, k, counts
