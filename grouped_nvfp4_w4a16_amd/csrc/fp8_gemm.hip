@@ -1162,7 +1162,9 @@ struct Plan {
 // cost 0.0205 us per row and step (0.0165 in the two larger tiles; the two-phase loop's rows
 // come in 64s), the FP8 products stay below the loads. An item costs 2 us more (its first
 // loads), 0.7 where two blocks fit a CU and one loads while the other starts, 1 where they
-// also join slice sums. A split adds a launch (6 with its wait) and writes and reads its sums,
+// also join slice sums; the two-stage SwiGLU tile alone on its CU takes 1.2 times its loads (70
+// slots over 107 experts, width 160 x K 3728: 35.6 us, 26.3 with three stages of 64 rows). A
+// split adds a launch (6 with its wait) and writes and reads its sums,
 // at 2.5 and 4 TB/s. HBM bounds all of it (the experts' weights at 6 TB/s); a tenth of the
 // estimate stands for what does not run beside that.
 //
@@ -1216,7 +1218,9 @@ Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, i
       double rounds = static_cast<double>(static_cast<int64_t>((items * ways + cus - 1) / cus));
       if (rounds < 1.0) rounds = 1.0;
       const double start = kSwiglu ? (t == 0 ? 0.7 : 2.0) : t < 2 ? 0.7 : t == 2 ? 2.0 : 1.0;
-      double us = rounds * (static_cast<double>((kb + ways - 1) / ways) * step + start);
+      const bool alone = kSwiglu && t == 0 && items * ways <= cus;  // on its CU
+      double us = rounds *
+                  (static_cast<double>((kb + ways - 1) / ways) * step * (alone ? 1.2 : 1.0) + start);
       us = 0.1 * us + (us < weights / 6e6 ? weights / 6e6 : us);
       if (ways > 1)
         us += 6.0 + static_cast<double>(ways) * rows * n * 8.0 * (1.0 / 2.5e6 + 1.0 / 4e6);
