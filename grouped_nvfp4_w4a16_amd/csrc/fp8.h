@@ -1,8 +1,8 @@
 // E4M3 (OCP FN) quantisation with one FP32 scale per 128 values, shared by the standalone
 // quantiser and the FP8 GEMMs' SwiGLU epilogue:
 //   scale = max(amax / 448, 2^-126),   code = e4m3_rne(value / scale),   in FP32.
-// Both divisions are IEEE, so a group's codes depend on its values alone (not on which
-// kernel wrote them). The floor keeps the scale a normal FP32 number: a group of zeros gets
+// Both quotients round as IEEE divisions do, so a group's codes depend on its values alone (not
+// on which kernel wrote them). The floor keeps the scale a normal FP32 number: a group of zeros gets
 // scale 2^-126 and codes 0. |value| / scale rounds to at most 448 (amax / 448 is off by half
 // an ulp at most), so no code saturates. A NaN in a group makes its scale and codes NaN; an
 // infinity makes the scale infinite, its own code NaN and the finite values' codes 0.

@@ -32,13 +32,13 @@
 //     workspace for a second launch (fp8_swiglu_finish_kernel).
 //
 // What bounds it and what it reaches (256 CUs, whole calls):
-//   - Many experts with few rows: HBM. 256 experts x 8 rows, N 6144 x K 2048: 534-557 us, 6.1
-//     of the 6.3 TB/s a plain read reaches; gate and up (2048 + 2048) x 6144: 1051 us, 6.1 TB/s.
+//   - Many experts with few rows: HBM. 256 experts x 8 rows, N 6144 x K 2048: 548 us, 5.9
+//     of the 6.3 TB/s a plain read reaches; gate and up (2048 + 2048) x 6144: 1063 us, 6.1 TB/s.
 //   - Large products: what a CU takes in through LDS (0.32 MB/us from its L2), since every row
 //     of 128 codes is read by one tile in N / BN (M / BT): 4096 x 6144 x 2048 in 67 us, 1540
 //     TFLOP/s. The 256 x 128 tile reads 48.5 KB per step and CU for 8.4 MFLOP.
 //   - SwiGLU, experts of 128 rows: conversions to BF16 and BF16 products on the same SIMDs.
-//     32768 slots over 256 experts, (2048 + 2048) x 6144: 2050 us, 800 TFLOP/s.
+//     32768 slots over 256 experts, (2048 + 2048) x 6144: 2026 us, 814 TFLOP/s.
 //   - One token: the chain of a launch, the first loads and the steps of one tile, 5.7 us of
 //     kernel at 1 x 6144 x 2048.
 #include <mutex>
@@ -1164,9 +1164,9 @@ struct Plan {
 // loads), 0.7 where two blocks fit a CU and one loads while the other starts, 1 where they
 // also join slice sums; the two-stage SwiGLU tile alone on its CU takes 1.2 times its loads (70
 // slots over 107 experts, width 160 x K 3728: 35.6 us, 26.3 with three stages of 64 rows). A
-// split adds a launch (6 with its wait) and writes and reads its sums,
-// at 2.5 and 4 TB/s. HBM bounds all of it (the experts' weights at 6 TB/s); a tenth of the
-// estimate stands for what does not run beside that.
+// split adds a launch (6 with its wait) and writes and reads its sums, at 2.5 and 4 TB/s. HBM
+// bounds all of it (the experts' weights at 6 TB/s); a tenth of the estimate stands for what
+// does not run beside that.
 //
 // Both sides, measured in us, the one taken marked:
 //   plain, N 6144 x K 2048            32 x 16   128 x 32   128 x 64   256 x 128
@@ -1181,12 +1181,12 @@ struct Plan {
 //   SwiGLU, width 2048 x K 6144       256 x 32   256 x 64   256 x 128   256 x 192
 //     256 experts, 8 rows each          1065*       1100
 //     256 experts, 32 rows each         1485        1237*
-//     256 experts, 128 rows each                    2858        2490        2050*
+//     256 experts, 128 rows each                    2858        2490        2026*
 //     4096 rows                                      279         194*        275
 //   (most of those experts of 128 rows pass 128 by a few: they would take two 128-row tiles)
 //   split of K, the same width            1          2          4           8
 //     8 rows, 256 x 32                  38.9       23.8       16.5        14.0*
-//     192 rows, 256 x 64                66.5       41.7       30.6*       36.7
+//     256 rows, 256 x 64                66.5       41.7       30.6*       36.7
 template <bool kSwiglu>
 Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, int cus) {
   const double used = experts > 0 ? static_cast<double>(experts < rows ? experts : rows) : 1.0;
