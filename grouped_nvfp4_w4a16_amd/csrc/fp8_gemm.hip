@@ -548,6 +548,8 @@ __device__ __forceinline__ void swiglu_epilogue(const GemmArgs &p, const Item &i
 
 template <class C, bool kGrouped>
 int lds_bytes(const GemmArgs &p) {
+  static_assert(C::kSbOff + 4 * C::kNBlocks * (kMaxK / kFp8Block + C::KS) +
+                    4 * (kMaxExperts + 16) <= 160 * 1024, "every size the checks allow fits");
   const int kb = (p.k + kFp8Block - 1) / kFp8Block;
   const int kb_pad = (kb + C::KS - 1) / C::KS * C::KS;
   return C::kSbOff + 4 * C::kNBlocks * kb_pad + (kGrouped ? 4 * (p.num_experts + 16) : 0);
