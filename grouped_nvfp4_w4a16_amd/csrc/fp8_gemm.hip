@@ -34,7 +34,7 @@
 // What bounds it and what it reaches (256 CUs, whole calls):
 //   - Many experts with few rows: HBM. 256 experts x 8 rows, N 6144 x K 2048: 548 us, 5.9
 //     of the 6.3 TB/s a plain read reaches; gate and up (2048 + 2048) x 6144: 1063 us, 6.1 TB/s.
-//   - Large products: what a CU takes in through LDS (0.32 MB/us from its L2), since every row
+//   - Large products: what a CU takes in through LDS (41 KB/us from its L2), since every row
 //     of 128 codes is read by one tile in N / BN (M / BT): 4096 x 6144 x 2048 in 67 us, 1540
 //     TFLOP/s. The 256 x 128 tile reads 48.5 KB per step and CU for 8.4 MFLOP.
 //   - SwiGLU, experts of 128 rows: conversions to BF16 and BF16 products on the same SIMDs.
@@ -1158,7 +1158,7 @@ struct Plan {
 };
 
 // Which tile, and how many splits of K (SwiGLU with a workspace only): the least of an
-// estimate in microseconds, from two measured rates. A CU takes in about 0.32 MB/us
+// estimate in microseconds, from two measured rates. A CU takes in about 41 KB/us
 // (0.0031 us per LDS row of 128 bytes; 64 KB in flight and any tile shape end there), so a
 // step costs 0.0031 us x (weight rows + rows); the SwiGLU form's conversions and BF16 products
 // cost 0.0205 us per row and step (0.0165 in the two larger tiles; the two-phase loop's rows
