@@ -1163,12 +1163,14 @@ struct Plan {
 // step costs 0.0031 us x (weight rows + rows); the SwiGLU form's conversions and BF16 products
 // cost 0.0205 us per row and step (0.0165 in the two larger tiles; the two-phase loop's rows
 // come in 64s), the FP8 products stay below the loads. An item costs 2 us more (its first
-// loads), 0.7 where two blocks fit a CU and one loads while the other starts, 1 where they
-// also join slice sums; the two-stage SwiGLU tile alone on its CU takes 1.2 times its loads (70
-// slots over 107 experts, width 160 x K 3728: 35.6 us, 26.3 with three stages of 64 rows). A
+// loads; 2.5 in the plain 256 x 128 tile), 0.7 where two blocks fit a CU and one loads while the
+// other starts, 1 where they also join slice sums (whose steps of four slices take 0.9). The
+// two-stage SwiGLU tile takes 1.1 times its step and 1.5 us an item (70 slots over 107 experts,
+// width 160 x K 3728: 35.6 us, 26.3 with three stages of 64 rows). A
 // split adds a launch (6 with its wait) and writes and reads its sums, at 2.5 and 4 TB/s. HBM
 // bounds all of it (the experts' weights at 6 TB/s); a tenth of the estimate stands for what
-// does not run beside that.
+// does not run beside that. Over 400 random sizes the choice is 1.2 to 2.4 % slower than the
+// best (geometric mean; dense 1.2, dense SwiGLU 1.3, grouped SwiGLU 2.2, grouped 2.4).
 //
 // Both sides, measured in us, the one taken marked:
 //   plain, N 6144 x K 2048            32 x 16   128 x 32   128 x 64   256 x 128
@@ -1181,8 +1183,8 @@ struct Plan {
 //     256 experts, 32 rows each         1278         648        605*        607
 //     256 experts, 128 rows each        3985        1518       1227         896*
 //   SwiGLU, width 2048 x K 6144       256 x 32   256 x 64   256 x 128   256 x 192
-//     256 experts, 8 rows each          1065*       1100
-//     256 experts, 32 rows each         1485        1237*
+//     256 experts, 8 rows each     1064-1105  1073-1080*
+//     256 experts, 32 rows each         1365        1183*
 //     256 experts, 128 rows each                    2858        2490        2026*
 //     4096 rows                                      279         194*        275
 //   (most of those experts of 128 rows pass 128 by a few: they would take two 128-row tiles)
@@ -1209,20 +1211,20 @@ Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, i
     if (tiles > avg) tiles = avg;
     const double live = experts > 0 ? avg / tiles : (avg < bt ? avg : bt);
     double step = 0.0031 * (width + live);
+    if (!kSwiglu && t == 3) step *= 0.9;
     if (kSwiglu) {
       const double rows_done = t != 2 ? live : live > 64 ? 128 : 64;
       const double compute = (t < 2 ? 0.0205 : 0.0165) * rows_done;
       if (compute > step) step = compute;
+      if (t == 0) step *= 1.1;
     }
     const double items = used * tiles * static_cast<double>((n + bn_out - 1) / bn_out);
     for (int ways = 1; ways <= (kSwiglu && split ? 8 : 1); ways *= 2) {
       if (ways > 1 && (items * ways > 1.5 * cus || kb < 3 * ways)) break;
       double rounds = static_cast<double>(static_cast<int64_t>((items * ways + cus - 1) / cus));
       if (rounds < 1.0) rounds = 1.0;
-      const double start = kSwiglu ? (t == 0 ? 0.7 : 2.0) : t < 2 ? 0.7 : t == 2 ? 2.0 : 1.0;
-      const bool alone = kSwiglu && t == 0 && items * ways <= cus;  // on its CU
-      double us = rounds *
-                  (static_cast<double>((kb + ways - 1) / ways) * step * (alone ? 1.2 : 1.0) + start);
+      const double start = kSwiglu ? (t == 0 ? 1.5 : 2.0) : t < 2 ? 0.7 : t == 2 ? 2.5 : 1.0;
+      double us = rounds * (static_cast<double>((kb + ways - 1) / ways) * step + start);
       us = 0.1 * us + (us < weights / 6e6 ? weights / 6e6 : us);
       if (ways > 1)
         us += 6.0 + static_cast<double>(ways) * rows * n * 8.0 * (1.0 / 2.5e6 + 1.0 / 4e6);
