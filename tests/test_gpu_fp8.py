@@ -240,6 +240,43 @@ def test_dense_strided_operands(hip):
     assert np.array_equal(_bf16_f64(c), codecs.round_bf16(fp8.product(a, sa, w, sw)))
 
 
+def test_offsets_past_32_bits(hip):
+    """Operands and outputs over 4 GiB: 16 rows again and again must give the same 16 outputs."""
+    rng = np.random.default_rng(40)
+    times, n, k = 40000, 144, 6912
+    m = 16 * times
+    a, sa = _int_operand(rng, 16, k, False)
+    w, sw = _int_operand(rng, n, k, True)
+    want = torch.from_numpy(codecs.round_bf16(fp8.product(a, sa, w, sw))).cuda().to(torch.bfloat16)
+    big_a = _dev(a).repeat(times, 1).view(torch.float8_e4m3fn)
+    big_sa = _dev(sa).repeat(times, 1)
+    assert big_a.numel() > 2 ** 32
+    buf = torch.zeros(m, 4096, dtype=torch.bfloat16, device="cuda")
+    c = buf[:, 3584:3584 + n]
+    assert c.stride(0) * m * 2 > 2 ** 32
+    hip.moe_dense_gemm_fp8(big_a, big_sa, _f8(w), _dev(sw), c)
+    assert torch.equal(c.view(times, 16, n), want.expand(times, 16, n))
+    buf.zero_()
+    table = _table(hip, [(w, sw), None, (w, sw)], n, k)
+    off = torch.tensor([0, m // 2, m // 2 + 16, m], dtype=torch.int32, device="cuda")
+    hip.moe_w8a8_grouped_gemm(big_a, big_sa, table, off, c)
+    got = c.view(times, 16, n)
+    assert torch.equal(got[:times // 2], want.expand(times // 2, 16, n))
+    assert not bool(got[times // 2].any())
+    assert torch.equal(got[times // 2 + 1:], want.expand(times // 2 - 1, 16, n))
+    del buf, c, got, big_sa
+    act = big_a.view(torch.uint8)  # quantised into
+    x = torch.randn(16, k, device="cuda").to(torch.bfloat16)
+    xs = x.repeat(times, 1)
+    scale = torch.empty(m, fp8.blocks(k), device="cuda")
+    hip.moe_quant_fp8(xs, act, scale)
+    q1 = torch.empty(16, k, dtype=torch.uint8, device="cuda")
+    s1 = torch.empty(16, fp8.blocks(k), device="cuda")
+    hip.moe_quant_fp8(x, q1, s1)
+    assert torch.equal(act.view(times, 16, k), q1.expand(times, 16, k))
+    assert torch.equal(scale.view(times, 16, -1), s1.expand(times, 16, s1.shape[1]))
+
+
 def test_dense_nan_and_infinity_stay_in_their_row(hip):
     rng = np.random.default_rng(10)
     m, n, k = 40, 144, 400
@@ -539,6 +576,15 @@ def test_grouped_swiglu(hip, experts, tokens, top_k, mi, k, kind):
                               _swiglu_rel(*src, gate, up, ref[live], limit))
     assert _rest_is(qb, POISON8, rows, mi, written)
     assert _rest_is(sb, -7.0, rows, fp8.blocks(mi), written)
+
+
+@pytest.mark.parametrize("k", [16, 112, 128, 240])
+def test_few_k_on_large_tiles(hip, k):
+    """Fewer steps than the large tiles have stages: one block of k, one that is partial, two."""
+    test_dense_exact_sums(hip, 4200, 2064, k)
+    test_dense_swiglu(hip, 4300, 400, k)
+    test_grouped_exact_sums(hip, 6, 3000, 2064, k, "skew", True)
+    test_grouped_swiglu(hip, 70, 4500, 2, 272, k, "even")
 
 
 def test_grouped_swiglu_split_leaves_uncovered_rows(hip):
