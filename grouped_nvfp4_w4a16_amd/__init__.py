@@ -212,9 +212,10 @@ def _bf16_matrix(t, name):
 
     if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
         raise TypeError(f"{name}: expected BF16 data, got {t.dtype}")
-    if t.dim() != 2 or t.stride(1) != 1:
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1:
         raise ValueError(f"{name}: expected a row-major 2-D tensor")
-    return t, t.stride(0)
+    return t, stride[0]
 
 
 # ------------------------------------------------------------------------------- calls
@@ -698,7 +699,7 @@ def moe_quant_fp8(x, q, scale, stream=None) -> None:
     x, ld_x = _bf16_matrix(x, "x")
     ld_q = _fp8_matrix(q, "q")
     rows, cols = x.shape
-    if tuple(q.shape) != (rows, cols):
+    if q.shape != x.shape:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
     ld_s = _scale_matrix(scale, rows, _fp8_blocks(cols), "scale")
     _same_device(x, q, scale)
