@@ -16,15 +16,16 @@
 // Structure:
 //   - A block owns BN weight rows x BT rows over the whole K, in stages of KS slices of 128 k
 //     loaded straight into LDS (buffer_load ... lds), ST - 1 stages ahead. LDS rows are
-//     128 bytes, 16-byte piece c of row r at c ^ (r & 7): the operand reads are conflict-free.
+//     128 bytes, 16-byte piece c of row r at c ^ (r & 7): the reads of 16-row operands are conflict-free
+//     (those of the two-phase loop's 32 rows are not; it is bound elsewhere).
 //   - Waves: WN x WT over the tile, and KS groups that split the slices of a stage (the small
 //     tiles, whose sums are then joined in slice order).
 //   - Rows past the tile's valid ones, gather indices out of range and k past the end read
 //     zeros through their offset (past the buffer's end), without memory traffic.
-//   - Blocks are persistent: an item is a row tile x a weight tile, each XCD takes a contiguous
-//     eighth of the items and its blocks take them in turn. Grouped form: a block counts the
-//     experts' row tiles from the offsets once (a prefix sum kept in LDS): only experts with
-//     rows cost anything, however the rows are routed.
+//   - Blocks are persistent: an item is a row tile x a weight tile, neighbouring items run on
+//     one XCD (Share). Grouped form: a block counts the experts' row tiles from the offsets once
+//     and takes them by falling size (Items): only experts with rows cost anything, however
+//     the rows are routed.
 //   - SwiGLU form: the tile's weight rows are 128 gate rows and the same 128 up rows, a wave
 //     holding both sums of an output; one block so owns whole 128-column groups of the
 //     output and quantises them in its epilogue. Nothing is rounded between the FP32 sums and
@@ -33,12 +34,12 @@
 //
 // What bounds it and what it reaches (256 CUs, whole calls):
 //   - Many experts with few rows: HBM. 256 experts x 8 rows, N 6144 x K 2048: 548 us, 5.9
-//     of the 6.3 TB/s a plain read reaches; gate and up (2048 + 2048) x 6144: 1063 us, 6.1 TB/s.
-//   - Large products: what a CU takes in through LDS (41 KB/us from its L2), since every row
-//     of 128 codes is read by one tile in N / BN (M / BT): 4096 x 6144 x 2048 in 67 us, 1540
+//     of the 6.3 TB/s a plain read reaches; gate and up (2048 + 2048) x 6144: 1038 us, 6.2 TB/s.
+//   - Large products: what a CU takes in through LDS (41 KB/us from its L2), since N / BN
+//     tiles read every row and M / BT every weight: 4096 x 6144 x 2048 in 65-71 us, 1440-1600
 //     TFLOP/s. The 256 x 128 tile reads 48.5 KB per step and CU for 8.4 MFLOP.
 //   - SwiGLU, experts of 128 rows: conversions to BF16 and BF16 products on the same SIMDs.
-//     32768 slots over 256 experts, (2048 + 2048) x 6144: 2026 us, 814 TFLOP/s.
+//     32768 slots over 256 experts, (2048 + 2048) x 6144: 2026-2146 us, 770-814 TFLOP/s.
 //   - One token: the chain of a launch, the first loads and the steps of one tile, 5.7 us of
 //     kernel at 1 x 6144 x 2048.
 #include <mutex>
