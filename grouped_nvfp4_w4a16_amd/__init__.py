@@ -683,11 +683,15 @@ def _fp8_blocks(n):
     return -(-n // FP8_BLOCK)
 
 
-def _same_device(*tensors):
-    """Raises unless every tensor lies on the current device (the launch goes there)."""
+def _same_device(stream, *tensors):
+    """Raises unless the stream and every tensor belong to the current device (the launch is
+    prepared for it and goes there)."""
     import torch
 
     dev = torch._C._cuda_getDevice()
+    at = dev if stream is None else getattr(stream, "device_index", dev)
+    if at != dev:
+        raise ValueError(f"the stream belongs to cuda:{at}, the current device is cuda:{dev}")
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor lies on {t.device}, the current device is cuda:{dev}")
@@ -702,7 +706,7 @@ def moe_quant_fp8(x, q, scale, stream=None) -> None:
     if q.shape != x.shape:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
     ld_s = _scale_matrix(scale, rows, _fp8_blocks(cols), "scale")
-    _same_device(x, q, scale)
+    _same_device(stream, x, q, scale)
     _check("moe_quant_fp8", load().moe_quant_fp8(
         _p(x), ld_x, _p(q), ld_q, _p(scale), ld_s, rows, cols, _stream(stream)))
 
@@ -721,7 +725,7 @@ def moe_dense_gemm_fp8(a, a_scale, b, b_scale, c, stream=None) -> None:
     kb = _fp8_blocks(k)
     ld_as = _scale_matrix(a_scale, m, kb, "a_scale")
     _scale_matrix(b_scale, _fp8_blocks(n), kb, "b_scale", contiguous=True)
-    _same_device(a, a_scale, b, b_scale, c)
+    _same_device(stream, a, a_scale, b, b_scale, c)
     _check("moe_dense_gemm_fp8", load().moe_dense_gemm_fp8(
         _p(a), lda, _p(a_scale), ld_as, _p(b), ldb, _p(b_scale), _p(c), ldc, m, n, k,
         _stream(stream)))
@@ -742,7 +746,7 @@ def _swiglu_workspace(ws, rows, num_experts, width, k, device, stream):
 
     if ws is not None:
         wp, wb = _workspace(ws)
-        _same_device(ws)
+        _same_device(stream, ws)
         return ws, wp, wb
     need = load().moe_fp8_swiglu_workspace_bytes(rows, num_experts, width, k)
     if need == 0:
@@ -776,7 +780,7 @@ def moe_dense_gate_up_swiglu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale,
     _scale_matrix(gate_scale, ib, kb, "gate_scale", contiguous=True)
     _scale_matrix(up_scale, ib, kb, "up_scale", contiguous=True)
     ld_os = _scale_matrix(act_scale, m, ib, "act_scale")
-    _same_device(a, a_scale, gate_w, gate_scale, up_w, up_scale, act, act_scale)
+    _same_device(stream, a, a_scale, gate_w, gate_scale, up_w, up_scale, act, act_scale)
     ws, wp, wb = _swiglu_workspace(workspace, m, 0, inter, k, a.device, stream)
     _check("moe_dense_gate_up_swiglu_fp8", load().moe_dense_gate_up_swiglu_fp8(
         _p(a), lda, _p(a_scale), ld_as, _p(gate_w), _p(gate_scale), _p(up_w), _p(up_scale), ldw,
@@ -815,7 +819,7 @@ def moe_w8a8_grouped_gemm(a, a_scale, table: "Fp8ExpertTable", expert_offsets, c
         raise ValueError("a gate_up table goes to moe_w8a8_grouped_gemm_swiglu")
     if c.shape[1] < table.n:
         raise ValueError("c too narrow for the table's n")
-    _same_device(a, a_scale, expert_offsets, c, a_gather, table.weight_ptrs)
+    _same_device(stream, a, a_scale, expert_offsets, c, a_gather, table.weight_ptrs)
     _check("moe_w8a8_grouped_gemm", load().moe_w8a8_grouped_gemm(
         _p(a), lda, _p(a_scale), ld_as, a.shape[0], _p(a_gather), _p(table.weight_ptrs),
         _p(table.scale_ptrs), _p(expert_offsets), table.num_experts, _p(c), ldc, rows, table.n,
@@ -839,7 +843,7 @@ def moe_w8a8_grouped_gemm_swiglu(a, a_scale, table: "Fp8ExpertTable", expert_off
     if act.shape[1] < mi:
         raise ValueError("act too narrow for the table's n / 2")
     ld_os = _scale_matrix(act_scale, rows, _fp8_blocks(mi), "act_scale")
-    _same_device(a, a_scale, expert_offsets, act, act_scale, a_gather, table.weight_ptrs)
+    _same_device(stream, a, a_scale, expert_offsets, act, act_scale, a_gather, table.weight_ptrs)
     ws, wp, wb = _swiglu_workspace(workspace, rows, table.num_experts, mi, table.k, a.device,
                                    stream)
     _check("moe_w8a8_grouped_gemm_swiglu", load().moe_w8a8_grouped_gemm_swiglu(
@@ -1235,6 +1239,7 @@ def moe_layer_fp8(x, topk_ids, topk_weights, gate_up: Fp8ExpertTable, down: Fp8E
         raise ValueError("the workspace was made for other sizes")
     if tuple(x.shape) != (rows, hidden) or tuple(out.shape) != (rows, hidden):
         raise ValueError(f"x and out must be [{rows}, {hidden}]")
+    _same_device(stream, x, topk_ids, topk_weights, out, ws.x)  # before the first launch
     s = rows * top_k
     moe_align(topk_ids, gate_up.num_experts, ws.sorted_token_ids, ws.sorted_expert_ids,
               ws.expert_offsets, ws.token_to_perm, None, None, stream,

@@ -1,0 +1,152 @@
+"""The FP8 calls of the Python binding on the host: stand-ins for device tensors, streams and
+the library show which arguments a call hands on, and that it refuses the others before
+anything reaches the GPU."""
+
+import pytest
+import torch
+
+import grouped_nvfp4_w4a16_amd as pkg
+
+F8, BF16, F32, I32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
+
+
+class Tensor:
+    """As much of a device tensor as the binding asks for; it holds no memory."""
+
+    is_cuda = True
+
+    def __init__(self, shape, dtype, stride=None, device=0, ptr=0x10000):
+        self.shape, self.dtype, self.index, self.ptr = torch.Size(shape), dtype, device, ptr
+        dense, n = [], 1
+        for d in reversed(self.shape):
+            dense.insert(0, n)
+            n *= d
+        self.strides = tuple(dense) if stride is None else tuple(stride)
+        self.dense = self.strides == tuple(dense)
+
+    def stride(self, dim=None):
+        return self.strides if dim is None else self.strides[dim]
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def is_contiguous(self):
+        return self.dense
+
+    def get_device(self):
+        return self.index
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.index)
+
+    def data_ptr(self):
+        return self.ptr
+
+
+class Library:
+    """Records every call's arguments; each succeeds."""
+
+    def __init__(self):
+        self.calls = []
+
+    def moe_fp8_swiglu_workspace_bytes(self, *args):
+        return 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+class Table:
+    """An Fp8ExpertTable's fields."""
+
+    def __init__(self, experts, n, k, gate_up=False, device=0):
+        self.n, self.k, self.num_experts, self.gate_up = n, k, experts, gate_up
+        self.present = [True] * experts
+        self.weight_ptrs = Tensor((experts,), torch.int64, device=device)
+        self.scale_ptrs = Tensor((experts,), torch.int64, device=device)
+
+
+class Stream:
+    def __init__(self, device_index, handle=0x77):
+        self.device_index, self.cuda_stream = device_index, handle
+
+
+@pytest.fixture
+def lib(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(pkg, "load", lambda: lib)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x55, raising=False)
+    return lib
+
+
+def _quant(rows=4, cols=256, **kw):
+    pkg.moe_quant_fp8(Tensor((rows, cols), BF16), Tensor((rows, cols), F8),
+                      Tensor((rows, -(-cols // 128)), F32), **kw)
+
+
+def _dense(m=4, n=144, k=256, **kw):
+    pkg.moe_dense_gemm_fp8(Tensor((m, k), F8), Tensor((m, 2), F32), Tensor((n, k), F8),
+                           Tensor((-(-n // 128), 2), F32), Tensor((m, n), BF16), **kw)
+
+
+def _dense_swiglu(m=4, n=144, k=256, **kw):
+    w, s = Tensor((n, k), F8), Tensor((2, 2), F32)
+    pkg.moe_dense_gate_up_swiglu_fp8(Tensor((m, k), F8), Tensor((m, 2), F32), w, s, w, s,
+                                     Tensor((m, n), F8), Tensor((m, 2), F32), 7.0, **kw)
+
+
+def _grouped(rows=4, **kw):
+    pkg.moe_w8a8_grouped_gemm(Tensor((rows, 256), F8), Tensor((rows, 2), F32), Table(3, 144, 256),
+                              Tensor((4,), I32), Tensor((rows, 144), BF16), **kw)
+
+
+def _grouped_swiglu(rows=4, **kw):
+    pkg.moe_w8a8_grouped_gemm_swiglu(Tensor((rows, 256), F8), Tensor((rows, 2), F32),
+                                     Table(3, 288, 256, True), Tensor((4,), I32),
+                                     Tensor((rows, 144), F8), Tensor((rows, 2), F32), 7.0, **kw)
+
+
+CALLS = {"moe_quant_fp8": _quant, "moe_dense_gemm_fp8": _dense,
+         "moe_dense_gate_up_swiglu_fp8": _dense_swiglu, "moe_w8a8_grouped_gemm": _grouped,
+         "moe_w8a8_grouped_gemm_swiglu": _grouped_swiglu}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_the_stream_of_a_call(lib, name):
+    """The current device's current stream, or the given one; a stream of another device would
+    run a kernel prepared for the current one, on memory of the current one: refused."""
+    CALLS[name]()
+    CALLS[name](stream=Stream(0))
+    assert [(n, a[-1]) for n, a in lib.calls] == [(name, 0x55), (name, 0x77)]
+    with pytest.raises(ValueError, match="stream"):
+        CALLS[name](stream=Stream(1))
+    assert len(lib.calls) == 2
+
+
+class Workspace:
+    """An Fp8Workspace's fields for 4 rows, top 2 of 3 experts, hidden 256, width 144."""
+
+    max_rows, top_k, num_experts, hidden, moe_intermediate = 4, 2, 3, 256, 144
+
+    def __init__(self, device=0):
+        self.x = Tensor((4, 256), F8, device=device)
+
+
+@pytest.mark.parametrize("case", ["stream", "x", "workspace"])
+def test_a_layer_on_another_device_launches_nothing(lib, case):
+    at = {case: 1}
+    ids, w = Tensor((4, 2), I32), Tensor((4, 2), F32)
+    with pytest.raises(ValueError, match="cuda:1"):
+        pkg.moe_layer_fp8(Tensor((4, 256), BF16, device=at.get("x", 0)), ids, w,
+                          Table(3, 288, 256, True), Table(3, 256, 144), 7.0,
+                          Workspace(at.get("workspace", 0)), Tensor((4, 256), BF16),
+                          stream=Stream(at.get("stream", 0)))
+    assert lib.calls == []
