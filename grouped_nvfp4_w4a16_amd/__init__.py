@@ -683,6 +683,13 @@ def _fp8_blocks(n):
     return -(-n // FP8_BLOCK)
 
 
+def _fits_int32(*sizes):
+    """Raises unless the library's 32-bit sizes hold these (ctypes would cut them)."""
+    for n in sizes:
+        if not -0x80000000 <= n <= 0x7FFFFFFF:
+            raise ValueError(f"{n} is no 32-bit size")
+
+
 def _same_device(stream, *tensors):
     """Raises unless the stream and every tensor belong to the current device (the launch is
     prepared for it and goes there)."""
@@ -705,6 +712,7 @@ def moe_quant_fp8(x, q, scale, stream=None) -> None:
     rows, cols = x.shape
     if q.shape != x.shape:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
+    _fits_int32(rows, cols)
     ld_s = _scale_matrix(scale, rows, _fp8_blocks(cols), "scale")
     _same_device(stream, x, q, scale)
     _check("moe_quant_fp8", load().moe_quant_fp8(
@@ -722,6 +730,7 @@ def moe_dense_gemm_fp8(a, a_scale, b, b_scale, c, stream=None) -> None:
     if kw != k or c.shape != (m, n):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, "
                          f"c {tuple(c.shape)}")
+    _fits_int32(m, n, k)
     kb = _fp8_blocks(k)
     ld_as = _scale_matrix(a_scale, m, kb, "a_scale")
     _scale_matrix(b_scale, _fp8_blocks(n), kb, "b_scale", contiguous=True)
@@ -735,8 +744,9 @@ def moe_fp8_swiglu_workspace_bytes(rows: int, num_experts: int, width: int, k: i
     """Bytes of the workspace moe_w8a8_grouped_gemm_swiglu (``width`` = mi) or, with
     ``num_experts`` 0, moe_dense_gate_up_swiglu_fp8 (``width`` = inter) splits these sizes
     with; 0 where they are not split."""
-    return int(load().moe_fp8_swiglu_workspace_bytes(int(rows), int(num_experts), int(width),
-                                                     int(k)))
+    rows, num_experts, width, k = int(rows), int(num_experts), int(width), int(k)
+    _fits_int32(rows, num_experts, width, k)
+    return int(load().moe_fp8_swiglu_workspace_bytes(rows, num_experts, width, k))
 
 
 def _swiglu_workspace(ws, rows, num_experts, width, k, device, stream):
@@ -775,6 +785,7 @@ def moe_dense_gate_up_swiglu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale,
     if gate_w.shape[1] != k or tuple(act.shape) != (m, inter):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, gate_w {tuple(gate_w.shape)}, "
                          f"act {tuple(act.shape)}")
+    _fits_int32(m, inter, k)
     kb, ib = _fp8_blocks(k), _fp8_blocks(inter)
     ld_as = _scale_matrix(a_scale, m, kb, "a_scale")
     _scale_matrix(gate_scale, ib, kb, "gate_scale", contiguous=True)
@@ -798,6 +809,7 @@ def _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows, out_rows):
     if expert_offsets.numel() < table.num_experts + 1 or not expert_offsets.is_contiguous():
         raise ValueError("expert_offsets: needs num_experts + 1 contiguous elements")
     rows = out_rows if max_rows is None else max_rows
+    _fits_int32(rows, a.shape[0], table.n, table.k)
     if rows > out_rows or (a_gather is not None and
                            (a_gather.numel() < rows or not a_gather.is_contiguous())):
         raise ValueError("max_rows exceeds the output or a_gather")

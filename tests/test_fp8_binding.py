@@ -150,3 +150,29 @@ def test_a_layer_on_another_device_launches_nothing(lib, case):
                           Workspace(at.get("workspace", 0)), Tensor((4, 256), BF16),
                           stream=Stream(at.get("stream", 0)))
     assert lib.calls == []
+
+
+BIG = 2 ** 32 + 16  # 16 in 32 bits
+
+
+@pytest.mark.parametrize("call", [
+    lambda: _quant(rows=BIG, cols=16), lambda: _quant(rows=1, cols=BIG), lambda: _dense(m=BIG),
+    lambda: _dense(n=BIG), lambda: _dense_swiglu(m=BIG), lambda: _grouped(rows=BIG),
+    lambda: _grouped_swiglu(rows=BIG), lambda: _grouped(max_rows=-BIG),
+    lambda: pkg.moe_fp8_swiglu_workspace_bytes(BIG, 0, 2048, 6144),
+    lambda: pkg.moe_fp8_swiglu_workspace_bytes(8, 0, BIG, 6144)])
+def test_sizes_past_32_bits_are_refused(lib, call):
+    """The library takes 32-bit sizes: a longer one must not be cut to its low bits."""
+    with pytest.raises(ValueError, match="32-bit"):
+        call()
+    assert lib.calls == []
+
+
+def test_gathered_rows_past_32_bits_are_refused(lib):
+    for grouped, table, out in ((pkg.moe_w8a8_grouped_gemm, Table(3, 144, 256), BF16),
+                                (pkg.moe_w8a8_grouped_gemm_swiglu, Table(3, 288, 256, True), F8)):
+        rest = () if out is BF16 else (Tensor((4, 2), F32), 7.0)
+        with pytest.raises(ValueError, match="32-bit"):
+            grouped(Tensor((BIG, 256), F8), Tensor((BIG, 2), F32), table, Tensor((4,), I32),
+                    Tensor((4, 144), out), *rest, a_gather=Tensor((4,), I32))
+    assert lib.calls == []
