@@ -664,6 +664,12 @@ def _fp8_matrix(t, name):
     return stride[0]
 
 
+def _row_stride(ld, shape):
+    """The leading dimension to pass for a matrix of this shape: of a single row the stride says
+    nothing, its width (up to a multiple of 16) stands for it."""
+    return ld if shape[0] > 1 else (shape[1] + 15) & -16
+
+
 def _scale_matrix(t, rows, cols, name, contiguous=False):
     """Leading dimension of a float32 [rows, cols] device tensor (at least)."""
     import torch
@@ -675,8 +681,7 @@ def _scale_matrix(t, rows, cols, name, contiguous=False):
         raise ValueError(f"{name}: needs {rows} x {cols} scales, rows contiguous")
     if contiguous and (shape[1] != cols or not t.is_contiguous()):
         raise ValueError(f"{name}: expected a contiguous [{rows}, {cols}] tensor")
-    # of a single row the stride says nothing
-    return stride[0] if shape[0] > 1 else max(stride[0], cols)
+    return stride[0] if shape[0] > 1 else max(cols, 1)  # a single row's stride says nothing
 
 
 def _fp8_blocks(n):
@@ -713,6 +718,7 @@ def moe_quant_fp8(x, q, scale, stream=None) -> None:
     if q.shape != x.shape:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
     _fits_int32(rows, cols)
+    ld_x, ld_q = _row_stride(ld_x, x.shape), _row_stride(ld_q, x.shape)
     ld_s = _scale_matrix(scale, rows, _fp8_blocks(cols), "scale")
     _same_device(stream, x, q, scale)
     _check("moe_quant_fp8", load().moe_quant_fp8(
@@ -731,6 +737,7 @@ def moe_dense_gemm_fp8(a, a_scale, b, b_scale, c, stream=None) -> None:
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, "
                          f"c {tuple(c.shape)}")
     _fits_int32(m, n, k)
+    lda, ldc = _row_stride(lda, (m, k)), _row_stride(ldc, (m, n))
     kb = _fp8_blocks(k)
     ld_as = _scale_matrix(a_scale, m, kb, "a_scale")
     _scale_matrix(b_scale, _fp8_blocks(n), kb, "b_scale", contiguous=True)
@@ -786,6 +793,7 @@ def moe_dense_gate_up_swiglu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale,
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, gate_w {tuple(gate_w.shape)}, "
                          f"act {tuple(act.shape)}")
     _fits_int32(m, inter, k)
+    lda, ld_act = _row_stride(lda, (m, k)), _row_stride(ld_act, (m, inter))
     kb, ib = _fp8_blocks(k), _fp8_blocks(inter)
     ld_as = _scale_matrix(a_scale, m, kb, "a_scale")
     _scale_matrix(gate_scale, ib, kb, "gate_scale", contiguous=True)
@@ -803,7 +811,7 @@ def _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows, out_rows):
     """Checks the row side of a grouped FP8 call; (lda, ld_a_scale, rows)."""
     import torch
 
-    lda = _fp8_matrix(a, "a")
+    lda = _row_stride(_fp8_matrix(a, "a"), a.shape)
     _want(expert_offsets, torch.int32, "expert_offsets")
     _want(a_gather, torch.int32, "a_gather")
     if expert_offsets.numel() < table.num_experts + 1 or not expert_offsets.is_contiguous():
@@ -831,6 +839,7 @@ def moe_w8a8_grouped_gemm(a, a_scale, table: "Fp8ExpertTable", expert_offsets, c
         raise ValueError("a gate_up table goes to moe_w8a8_grouped_gemm_swiglu")
     if c.shape[1] < table.n:
         raise ValueError("c too narrow for the table's n")
+    ldc = _row_stride(ldc, c.shape)
     _same_device(stream, a, a_scale, expert_offsets, c, a_gather, table.weight_ptrs)
     _check("moe_w8a8_grouped_gemm", load().moe_w8a8_grouped_gemm(
         _p(a), lda, _p(a_scale), ld_as, a.shape[0], _p(a_gather), _p(table.weight_ptrs),
@@ -854,6 +863,7 @@ def moe_w8a8_grouped_gemm_swiglu(a, a_scale, table: "Fp8ExpertTable", expert_off
     mi = table.n // 2
     if act.shape[1] < mi:
         raise ValueError("act too narrow for the table's n / 2")
+    ld_act = _row_stride(ld_act, act.shape)
     ld_os = _scale_matrix(act_scale, rows, _fp8_blocks(mi), "act_scale")
     _same_device(stream, a, a_scale, expert_offsets, act, act_scale, a_gather, table.weight_ptrs)
     ws, wp, wb = _swiglu_workspace(workspace, rows, table.num_experts, mi, table.k, a.device,

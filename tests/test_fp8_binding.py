@@ -176,3 +176,34 @@ def test_gathered_rows_past_32_bits_are_refused(lib):
             grouped(Tensor((BIG, 256), F8), Tensor((BIG, 2), F32), table, Tensor((4,), I32),
                     Tensor((4, 144), out), *rest, a_gather=Tensor((4,), I32))
     assert lib.calls == []
+
+
+@pytest.mark.parametrize("stride", [(1, 1), (0, 1), (258, 1), (1 << 23, 1)])
+def test_a_single_rows_stride_says_nothing(lib, stride):
+    """One row of a matrix of any stride (odd, zero, past 2^22): where its rows would go on does
+    not matter."""
+    def row(cols, dtype):
+        return Tensor((1, cols), dtype, stride)
+
+    one = Tensor((1, 2), F32, stride)
+    pkg.moe_quant_fp8(row(256, BF16), row(256, F8), one)
+    pkg.moe_dense_gemm_fp8(row(256, F8), one, Tensor((144, 256), F8), Tensor((2, 2), F32),
+                           row(144, BF16))
+    w, s = Tensor((144, 256), F8), Tensor((2, 2), F32)
+    pkg.moe_dense_gate_up_swiglu_fp8(row(256, F8), one, w, s, w, s, row(144, F8), one, 7.0)
+    off = Tensor((4,), I32)
+    pkg.moe_w8a8_grouped_gemm(row(250, F8), one, Table(3, 144, 240), off, row(144, BF16))
+    pkg.moe_w8a8_grouped_gemm_swiglu(row(256, F8), one, Table(3, 288, 256, True), off,
+                                     row(144, F8), one, 7.0)
+    lds = {name: args for name, args in lib.calls}
+    assert lds["moe_quant_fp8"][1] == lds["moe_quant_fp8"][3] == 256
+    assert lds["moe_dense_gemm_fp8"][1] == 256 and lds["moe_dense_gemm_fp8"][8] == 144
+    assert lds["moe_dense_gate_up_swiglu_fp8"][1] == 256
+    assert lds["moe_dense_gate_up_swiglu_fp8"][10] == 144
+    assert lds["moe_w8a8_grouped_gemm"][1] == 256 and lds["moe_w8a8_grouped_gemm"][11] == 144
+    assert lds["moe_w8a8_grouped_gemm_swiglu"][11] == 144
+    assert lds["moe_quant_fp8"][5] == lds["moe_dense_gemm_fp8"][3] == 2
+    # of two rows it is what it is
+    pkg.moe_quant_fp8(Tensor((2, 256), BF16, (264, 1)), Tensor((2, 256), F8, (272, 1)),
+                      Tensor((2, 2), F32))
+    assert lib.calls[-1][1][1] == 264 and lib.calls[-1][1][3] == 272
