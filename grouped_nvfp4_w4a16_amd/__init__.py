@@ -721,6 +721,8 @@ def moe_quant_fp8(x, q, scale, stream=None) -> None:
     ld_x, ld_q = _row_stride(ld_x, x.shape), _row_stride(ld_q, x.shape)
     ld_s = _scale_matrix(scale, rows, _fp8_blocks(cols), "scale")
     _same_device(stream, x, q, scale)
+    if cols == 0:
+        return
     _check("moe_quant_fp8", load().moe_quant_fp8(
         _p(x), ld_x, _p(q), ld_q, _p(scale), ld_s, rows, cols, _stream(stream)))
 

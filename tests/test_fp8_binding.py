@@ -207,3 +207,13 @@ def test_a_single_rows_stride_says_nothing(lib, stride):
     pkg.moe_quant_fp8(Tensor((2, 256), BF16, (264, 1)), Tensor((2, 256), F8, (272, 1)),
                       Tensor((2, 2), F32))
     assert lib.calls[-1][1][1] == 264 and lib.calls[-1][1][3] == 272
+
+
+@pytest.mark.parametrize("rows", [0, 1, 4])
+def test_quantising_no_columns_does_nothing(lib, rows):
+    """A matrix without columns has no stride to speak of (torch gives 1)."""
+    empty = torch.empty(rows, 0)
+    pkg.moe_quant_fp8(Tensor((rows, 0), BF16, empty.stride()), Tensor((rows, 0), F8, empty.stride()),
+                      Tensor((rows, 0), F32, empty.stride()))
+    for _, args in lib.calls:
+        assert args[1] % 8 == 0 and args[3] % 16 == 0

@@ -36,3 +36,11 @@ def test_one_row_of_any_stride(hip, gap):
     plain = chain(lambda cols, dtype: torch.zeros((1, cols), dtype=dtype, device="cuda"))
     for got, want in zip(chain(row), plain):
         assert torch.equal(got, want)
+
+
+def test_quantising_no_columns(hip):
+    for rows in (0, 3):
+        hip.moe_quant_fp8(torch.empty((rows, 0), dtype=BF16, device="cuda"),
+                          torch.empty((rows, 0), dtype=F8, device="cuda"),
+                          torch.empty((rows, 0), device="cuda"))
+    torch.cuda.synchronize()
