@@ -1188,6 +1188,24 @@ class Fp8ExpertTable:
         self.present = [w is not None for w in weights]
 
 
+def _split_device(device):
+    import torch
+
+    return torch.cuda.device(device)
+
+
+def _split_workspace(row_counts, num_experts, width, k, device):
+    """The split-K workspace of a SwiGLU product for any of these row counts (the need does not
+    grow with the rows: a full chip is not split), None where none is split. At most 1.5 tiles
+    a CU are split, 75 MB of sums."""
+    import torch
+
+    query = load().moe_fp8_swiglu_workspace_bytes
+    with _split_device(device):
+        need = max((query(r, num_experts, width, k) for r in row_counts), default=0)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
 class Fp8Workspace:
     """Every buffer one FP8 layer call needs, allocated once for up to ``max_rows``. Calls
     that share a workspace must be ordered on one stream."""
@@ -1211,13 +1229,16 @@ class Fp8Workspace:
         self.act = torch.empty(s, moe_intermediate, **f8)
         self.act_scale = torch.empty(s, _fp8_blocks(moe_intermediate), **f32)
         self.expert_out = torch.empty(s, hidden, dtype=torch.bfloat16, device=device)
+        self.split = _split_workspace(range(top_k, s + 1, top_k), num_experts, moe_intermediate,
+                                      hidden, device)
 
 
 class SharedExpertFp8:
     """The shared expert in FP8: E4M3 ``gate_w``, ``up_w`` ``[I, H]`` and ``down_w`` ``[H, I]``
-    with their block scales, plus its activation and output buffers for up to ``max_rows``
-    rows. Calling it on quantised rows runs moe_dense_gate_up_swiglu_fp8 then
-    moe_dense_gemm_fp8 and returns the BF16 ``[rows, H]`` output view."""
+    with their block scales, plus its activation, split-K and output buffers for up to
+    ``max_rows`` rows. Calling it on quantised rows runs moe_dense_gate_up_swiglu_fp8 then
+    moe_dense_gemm_fp8 and returns the BF16 ``[rows, H]`` output view. Its calls must be ordered
+    on one stream."""
 
     def __init__(self, gate_w, gate_scale, up_w, up_scale, down_w, down_scale, max_rows: int):
         import torch
@@ -1233,6 +1254,7 @@ class SharedExpertFp8:
         self.act_scale = torch.empty(max_rows, _fp8_blocks(inter), dtype=torch.float32,
                                      device=dev)
         self.out = torch.empty(max_rows, hidden, dtype=torch.bfloat16, device=dev)
+        self.split = _split_workspace(range(1, max_rows + 1), 0, inter, hidden, dev)
 
     def __call__(self, x, x_scale, limit: float, stream=None):
         rows = x.shape[0]
@@ -1240,7 +1262,7 @@ class SharedExpertFp8:
             raise ValueError(f"{rows} rows exceed the {self.act.shape[0]} the buffers hold")
         act, act_scale, out = self.act[:rows], self.act_scale[:rows], self.out[:rows]
         moe_dense_gate_up_swiglu_fp8(x, x_scale, *self.gate, *self.up, act, act_scale, limit,
-                                     stream)
+                                     stream, self.split)
         moe_dense_gemm_fp8(act, act_scale, *self.down, out, stream)
         return out
 
@@ -1272,7 +1294,7 @@ def moe_layer_fp8(x, topk_ids, topk_weights, gate_up: Fp8ExpertTable, down: Fp8E
     moe_quant_fp8(x, xq, xs, stream)
     act, act_scale = ws.act[:s], ws.act_scale[:s]
     moe_w8a8_grouped_gemm_swiglu(xq, xs, gate_up, ws.expert_offsets, act, act_scale, limit,
-                                 ws.sorted_token_ids, stream=stream)
+                                 ws.sorted_token_ids, stream=stream, workspace=ws.split)
     moe_w8a8_grouped_gemm(act, act_scale, down, ws.expert_offsets, ws.expert_out[:s],
                           stream=stream)
     if isinstance(shared, SharedExpertFp8):

@@ -2,6 +2,8 @@
 the library show which arguments a call hands on, and that it refuses the others before
 anything reaches the GPU."""
 
+import contextlib
+
 import pytest
 import torch
 
@@ -217,3 +219,24 @@ def test_quantising_no_columns_does_nothing(lib, rows):
                       Tensor((rows, 0), F32, empty.stride()))
     for _, args in lib.calls:
         assert args[1] % 8 == 0 and args[3] % 16 == 0
+
+
+class Sized(Library):
+    """A library whose split workspace is largest in the middle of the row counts."""
+
+    def moe_fp8_swiglu_workspace_bytes(self, rows, experts, width, k):
+        return {0: 256, 1: 512}.get(abs(rows - (8 if experts else 4)), 0)
+
+
+def test_the_layer_holds_its_split_workspaces(monkeypatch):
+    """The largest need over every row count up to max_rows, which the last one may not be;
+    none where no row count splits."""
+    monkeypatch.setattr(pkg, "load", Sized)
+    monkeypatch.setattr(pkg, "_split_device", lambda device: contextlib.nullcontext())
+    assert pkg.Fp8Workspace(6, 2, 3, 256, 144, device="cpu").split.numel() == 256
+    assert pkg.Fp8Workspace(6, 3, 3, 256, 144, device="cpu").split.numel() == 512
+    assert pkg.Fp8Workspace(2, 2, 3, 256, 144, device="cpu").split is None
+    w, s = torch.empty(144, 256), torch.empty(2, 2)
+    for rows, need in ((9, 512), (3, 512), (1, None)):
+        sh = pkg.SharedExpertFp8(w, s, w, s, w.t().contiguous(), s, rows)
+        assert (None if sh.split is None else sh.split.numel()) == need

@@ -44,3 +44,39 @@ def test_quantising_no_columns(hip):
                           torch.empty((rows, 0), dtype=F8, device="cuda"),
                           torch.empty((rows, 0), device="cuda"))
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows", [1, 8, 60])
+def test_a_layer_call_allocates_nothing(hip, rows):
+    """Everything a layer with its shared expert needs, the split-K sums among it, lies in the
+    workspace objects; every row count up to theirs gives the bits of objects of its own size."""
+    torch.manual_seed(rows)
+    experts, top_k, hidden, mi, max_rows = 6, 2, 2064, 144, 70
+    assert hip.moe_fp8_swiglu_workspace_bytes(rows * top_k, experts, mi, hidden) > 0
+    assert hip.moe_fp8_swiglu_workspace_bytes(rows, 0, mi, hidden) > 0
+
+    def weight(n, k):
+        w = torch.randint(0, 120, (n, k), dtype=torch.uint8, device="cuda")
+        return w, torch.rand(-(-n // 128), -(-k // 128), device="cuda") / 1000
+
+    gu = [tuple(torch.cat(t) for t in zip(weight(mi, hidden), weight(mi, hidden)))
+          for _ in range(experts)]
+    dn = [weight(hidden, mi) for _ in range(experts)]
+    gt = hip.Fp8ExpertTable(*zip(*gu), 2 * mi, hidden, gate_up=True)
+    dt = hip.Fp8ExpertTable(*zip(*dn), hidden, mi)
+    sh_w = [t for w in (weight(mi, hidden), weight(mi, hidden), weight(hidden, mi)) for t in w]
+    x = torch.randn(rows, hidden, device="cuda").to(BF16)
+    ids = torch.rand(rows, experts, device="cuda").argsort(1)[:, :top_k].int().contiguous()
+    w = torch.rand(rows, top_k, device="cuda")
+    outs = []
+    for most in (max_rows, rows):
+        ws = hip.Fp8Workspace(most, top_k, experts, hidden, mi)
+        shared = hip.SharedExpertFp8(*sh_w, most)
+        out = torch.empty((rows, hidden), dtype=BF16, device="cuda")
+        hip.moe_layer_fp8(x, ids, w, gt, dt, 7.0, ws, out, shared)
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_stats()["allocation.all.allocated"]
+        hip.moe_layer_fp8(x, ids, w, gt, dt, 7.0, ws, out, shared)
+        assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+        outs.append(out)
+    assert torch.equal(*outs)
