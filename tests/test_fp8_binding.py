@@ -240,3 +240,16 @@ def test_the_layer_holds_its_split_workspaces(monkeypatch):
     for rows, need in ((9, 512), (3, 512), (1, None)):
         sh = pkg.SharedExpertFp8(w, s, w, s, w.t().contiguous(), s, rows)
         assert (None if sh.split is None else sh.split.numel()) == need
+
+
+def test_the_current_stream_without_torchs_short_cuts(lib, monkeypatch):
+    """torch's internal queries are a short cut: without them its public ones serve."""
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream(0, 0x99))
+    for name, call in CALLS.items():
+        call()
+        assert lib.calls[-1][0] == name and lib.calls[-1][1][-1] == 0x99
+    with pytest.raises(ValueError, match="cuda:1"):
+        _quant(stream=Stream(1))
