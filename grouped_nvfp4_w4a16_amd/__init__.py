@@ -189,23 +189,17 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _current_device():
-    """torch.cuda.current_device(), by torch's internal query where there is one."""
-    import torch
-
-    query = getattr(torch._C, "_cuda_getDevice", None)
-    return torch.cuda.current_device() if query is None else query()
-
-
 def _stream(stream):
     """The handle of the given stream or of the current one (torch's internal query, where there
-    is one, makes no Stream object)."""
+    is one, makes no Stream object: 0.4 us, 2.7 with one)."""
     import torch
 
     if stream is not None:
         return stream.cuda_stream
     query = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return torch.cuda.current_stream().cuda_stream if query is None else query(_current_device())
+    if query is None:
+        return torch.cuda.current_stream().cuda_stream
+    return query(torch.cuda.current_device())
 
 
 def _want(t, dtype, name):
@@ -709,7 +703,9 @@ def _fits_int32(*sizes):
 def _same_device(stream, *tensors):
     """Raises unless the stream and every tensor belong to the current device (the launch is
     prepared for it and goes there)."""
-    dev = _current_device()
+    import torch
+
+    dev = torch.cuda.current_device()
     at = dev if stream is None else getattr(stream, "device_index", dev)
     if at != dev:
         raise ValueError(f"the stream belongs to cuda:{at}, the current device is cuda:{dev}")

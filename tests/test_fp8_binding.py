@@ -84,7 +84,7 @@ class Stream:
 def lib(monkeypatch):
     lib = Library()
     monkeypatch.setattr(pkg, "load", lambda: lib)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0x55, raising=False)
     return lib
 
@@ -242,11 +242,9 @@ def test_the_layer_holds_its_split_workspaces(monkeypatch):
         assert (None if sh.split is None else sh.split.numel()) == need
 
 
-def test_the_current_stream_without_torchs_short_cuts(lib, monkeypatch):
-    """torch's internal queries are a short cut: without them its public ones serve."""
-    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
-        monkeypatch.delattr(torch._C, name)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+def test_the_current_stream_without_torchs_short_cut(lib, monkeypatch):
+    """torch's internal query is a short cut: without it the public one serves."""
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
     monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream(0, 0x99))
     for name, call in CALLS.items():
         call()
