@@ -12,9 +12,10 @@
 
 #include <cstdint>
 
+#include "fp8_plan.h"  // kFp8Block
+
 namespace moe {
 
-constexpr int kFp8Block = 128;  // values per scale
 constexpr float kE4m3Max = 448.0f;
 
 // The scale of a group whose largest magnitude has the FP32 bits `amax_bits` (the maximum

@@ -48,6 +48,7 @@
 #include "buffer_io.h"
 #include "common.h"
 #include "fp8.h"
+#include "fp8_plan.h"
 #include "nvfp4_decode.h"  // moe::pack_bf16x2
 
 namespace {
@@ -1092,7 +1093,7 @@ int compute_units(int device) {
   return cus[device];
 }
 
-// The tiles a launch can take, narrowest first.
+// The kernels of fp8_tile's tiles.
 template <bool kSwiglu>
 struct Tiles;
 template <>
@@ -1109,6 +1110,16 @@ struct Tiles<true> {
   using T2 = Cfg<4, 4, 4, 2, 1, 3, true>;  // 256 x 128, two-phase
   using T3 = Cfg<4, 6, 4, 2, 1, 3>;        // 256 x 192, tall
 };
+
+template <class C, bool kSwiglu, int t>
+constexpr bool kTileIs =
+    C::BT == moe::fp8_tile<kSwiglu>(t).rows && C::BN == moe::fp8_tile<kSwiglu>(t).width;
+template <bool kSwiglu, class T = Tiles<kSwiglu>>
+constexpr bool kTilesMatch = kTileIs<typename T::T0, kSwiglu, 0> &&
+                             kTileIs<typename T::T1, kSwiglu, 1> &&
+                             kTileIs<typename T::T2, kSwiglu, 2> &&
+                             kTileIs<typename T::T3, kSwiglu, 3>;
+static_assert(kTilesMatch<false> && kTilesMatch<true>, "the plan's tiles are the kernels'");
 
 bool raise_lds(void (*kern)(GemmArgs)) {
   return hipFuncSetAttribute(reinterpret_cast<const void *>(kern),
@@ -1154,105 +1165,18 @@ int run(const char *name, const GemmArgs &p, int device, void *stream) {
                      dim3(static_cast<unsigned>(grid)), dim3(C::kThreads), bytes, stream, p);
 }
 
-struct Plan {
-  int tile, ways;
-};
-
-// Which tile, and how many splits of K (SwiGLU with a workspace only): the least of an
-// estimate in microseconds, from two measured rates. A CU takes in about 41 KB/us
-// (0.0031 us per LDS row of 128 bytes; 64 KB in flight and any tile shape end there), so a
-// step costs 0.0031 us x (weight rows + rows); the SwiGLU form's conversions and BF16 products
-// cost 0.0205 us per row and step (0.0165 in the two larger tiles; the two-phase loop's rows
-// come in 64s), the FP8 products stay below the loads. An item costs 2 us more (its first
-// loads; 2.5 in the plain 256 x 128 tile), 0.7 where two blocks fit a CU and one loads while the
-// other starts, 1 where they also join slice sums (whose steps of four slices take 0.9). The
-// two-stage SwiGLU tile takes 1.1 times its step and 1.5 us an item (70 slots over 107 experts,
-// width 160 x K 3728: 35.6 us, 26.3 with three stages of 64 rows). A
-// split adds a launch (6 with its wait) and writes and reads its sums, at 2.5 and 4 TB/s. HBM
-// bounds all of it (the experts' weights at 6 TB/s); a tenth of the estimate stands for what
-// does not run beside that. Over 400 random sizes the choice is 1.2 to 2.4 % slower than the
-// best (geometric mean; dense 1.2, dense SwiGLU 1.3, grouped SwiGLU 2.2, grouped 2.4).
-//
-// Both sides, measured in us, the one taken marked:
-//   plain, N 6144 x K 2048            32 x 16   128 x 32   128 x 64   256 x 128
-//     1 row                              9.3*       10.7        9.9        14.4
-//     64 rows                            9.1*        9.7       12.7        15.0
-//     256 rows                          25.6        13.1*      13.5        19.5
-//     1024 rows                         90.8        35.5       28.3        23.1*
-//     4096 rows                          348         128       95.3        72.0*
-//     256 experts, 8 rows each           691         557*       562         561
-//     256 experts, 32 rows each         1278         648        605*        607
-//     256 experts, 128 rows each        3985        1518       1227         896*
-//   SwiGLU, width 2048 x K 6144       256 x 32   256 x 64   256 x 128   256 x 192
-//     256 experts, 8 rows each     1064-1105  1073-1080*
-//     256 experts, 32 rows each         1365        1183*
-//     256 experts, 128 rows each                    2858        2490        2026*
-//     4096 rows                                      279         194*        275
-//   (most of those experts of 128 rows pass 128 by a few: they would take two 128-row tiles)
-//   split of K, the same width            1          2          4           8
-//     8 rows, 256 x 32                  38.9       23.8       16.5        14.0*
-//     256 rows, 256 x 64                66.5       41.7       30.6*       36.7
-template <bool kSwiglu>
-Plan plan_for(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, int cus) {
-  const double used = experts > 0 ? static_cast<double>(experts < rows ? experts : rows) : 1.0;
-  const double avg = static_cast<double>(rows) / used;
-  const int64_t kb = (k + kFp8Block - 1) / kFp8Block;
-  const double weights = used * static_cast<double>(n) * static_cast<double>(k) * (kSwiglu ? 2 : 1);
-  Plan best = {0, 1};
-  double best_us = 1e30;
-  for (int t = 0; t < 4; ++t) {
-    using T = Tiles<kSwiglu>;
-    constexpr int kRows[4] = {T::T0::BT, T::T1::BT, T::T2::BT, T::T3::BT};
-    constexpr int kWidths[4] = {T::T0::BN, T::T1::BN, T::T2::BN, T::T3::BN};
-    const int bt = kRows[t], width = kWidths[t], bn_out = kSwiglu ? width / 2 : width;
-    // Row tiles per expert: exact for one matrix; for experts of `avg` rows on average, one
-    // where they seldom pass the tile, else half a tile more than the rows need.
-    double tiles = experts > 0 ? (avg <= 0.75 * bt ? 1.0 : avg / bt + 0.5)
-                               : static_cast<double>((rows + bt - 1) / bt);
-    if (tiles > avg) tiles = avg;
-    const double live = experts > 0 ? avg / tiles : (avg < bt ? avg : bt);
-    double step = 0.0031 * (width + live);
-    if (!kSwiglu && t == 3) step *= 0.9;
-    if (kSwiglu) {
-      const double rows_done = t != 2 ? live : live > 64 ? 128 : 64;
-      const double compute = (t < 2 ? 0.0205 : 0.0165) * rows_done;
-      if (compute > step) step = compute;
-      if (t == 0) step *= 1.1;
-    }
-    const double items = used * tiles * static_cast<double>((n + bn_out - 1) / bn_out);
-    for (int ways = 1; ways <= (kSwiglu && split ? 8 : 1); ways *= 2) {
-      if (ways > 1 && (items * ways > 1.5 * cus || kb < 3 * ways)) break;
-      double rounds = static_cast<double>(static_cast<int64_t>((items * ways + cus - 1) / cus));
-      if (rounds < 1.0) rounds = 1.0;
-      const double start = kSwiglu ? (t == 0 ? 1.5 : 2.0) : t < 2 ? 0.7 : t == 2 ? 2.5 : 1.0;
-      double us = rounds * (static_cast<double>((kb + ways - 1) / ways) * step + start);
-      us = 0.1 * us + (us < weights / 6e6 ? weights / 6e6 : us);
-      if (ways > 1)
-        us += 6.0 + static_cast<double>(ways) * rows * n * 8.0 * (1.0 / 2.5e6 + 1.0 / 4e6);
-      if (us < best_us) {
-        best_us = us;
-        best = {t, ways};
-      }
-    }
-  }
-  return best;
-}
-
-int64_t partial_bytes(const Plan &plan, int64_t rows, int64_t n) {
-  return plan.ways > 1 ? plan.ways * rows * n * 8 : 0;
-}
-
 template <bool kSwiglu, bool kGrouped>
 int dispatch(const char *name, GemmArgs p, void *workspace, int64_t workspace_bytes,
              void *stream) {
   const int device = current_device();
   MOE_REQUIRE_CODE((allow_lds<kSwiglu, kGrouped>(device)), MOE_ELAUNCH,
                    "%s: the device refuses 160 KB of LDS to a block", name);
-  const Plan plan = plan_for<kSwiglu>(p.rows, kGrouped ? p.num_experts : 0, p.n, p.k,
-                                      workspace != nullptr, compute_units(device));
+  const moe::Fp8Plan plan =
+      moe::fp8_plan<kSwiglu>(p.rows, kGrouped ? p.num_experts : 0, p.n, p.k, workspace != nullptr,
+                             compute_units(device));
   p.ways = plan.ways;
   if (plan.ways > 1) {
-    const int64_t need = partial_bytes(plan, p.rows, p.n);
+    const int64_t need = moe::fp8_partial_bytes(plan, p.rows, p.n);
     MOE_REQUIRE_CODE(workspace_bytes >= need, MOE_ECAPACITY,
                      "%s: a workspace of %lld bytes, these sizes need %lld", name,
                      static_cast<long long>(workspace_bytes), static_cast<long long>(need));
@@ -1436,7 +1360,7 @@ extern "C" int moe_w8a8_grouped_gemm_swiglu(
 extern "C" int64_t moe_fp8_swiglu_workspace_bytes(int32_t rows, int32_t num_experts,
                                                   int32_t width, int32_t k) {
   if (rows <= 0 || num_experts < 0 || width <= 0 || k <= 0) return 0;
-  const Plan plan =
-      plan_for<true>(rows, num_experts, width, k, true, compute_units(current_device()));
-  return partial_bytes(plan, rows, width);
+  const moe::Fp8Plan plan =
+      moe::fp8_plan<true>(rows, num_experts, width, k, true, compute_units(current_device()));
+  return moe::fp8_partial_bytes(plan, rows, width);
 }
