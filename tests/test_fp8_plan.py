@@ -73,3 +73,21 @@ def test_the_swiglu_lists_reach_every_tile_in_one_launch():
     grouped = [fp8_plan.plan(True, r, e, n, k) for e, r, n, k, _ in test_gpu_fp8_swiglu.GROUPED]
     for plans in (dense, grouped):
         assert {t for t, ways in plans if ways == 1} == {0, 1, 2, 3}
+
+
+def test_the_split_lists_are_what_they_say():
+    """Every tile in every number of splits it takes, dense and grouped (the dense 128-row tile
+    is not split in two), and with an empty last split."""
+    dense, grouped = test_gpu_fp8_swiglu.DENSE_SPLIT, test_gpu_fp8_swiglu.GROUPED_SPLIT
+    for c in dense:
+        assert fp8_plan.plan(True, c[2], 0, *c[3:]) == c[:2], c
+    for c in grouped:
+        assert fp8_plan.plan(True, c[3], c[2], *c[4:6]) == c[:2], c
+    everything, empty = {(t, w) for t in range(4) for w in (2, 4, 8)}, set()
+    assert {c[:2] for c in dense} == everything - {(2, 2)}
+    assert {c[:2] for c in grouped} == everything
+    for c in dense + grouped:
+        blocks = -(-c[-1 if c in dense else 5] // 128)
+        if -(-blocks // c[1]) * (c[1] - 1) >= blocks:
+            empty.add((c[0], c in dense))
+    assert empty == {(t, kind) for t in range(4) for kind in (True, False)} - {(2, False)}

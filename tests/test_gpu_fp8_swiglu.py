@@ -94,3 +94,53 @@ GROUPED = [(1, 1, 16, 16, "even"), (8, 6, 128, 272, "even"), (9, 99, 272, 656, "
 @pytest.mark.parametrize("experts,rows,mi,k,kind", GROUPED)
 def test_grouped(hip, experts, rows, mi, k, kind, exact):
     run_grouped(hip, experts, rows, mi, k, kind, exact)
+
+
+# Sizes that split K, with the tile and the number of splits each takes (the launcher's rule on
+# 256 CUs, pinned on the CPU). Where ways - 1 splits already hold every block of 128 k (25 and 49
+# blocks in 8 parts), the last one is empty.
+DENSE_SPLIT = [  # tile, ways, m, n, k
+    (0, 2, 1034, 144, 1696), (0, 4, 1, 144, 1424), (0, 8, 1, 2048, 6144), (0, 8, 1, 144, 3088),
+    (0, 8, 8, 272, 2960), (1, 2, 2053, 144, 3664), (1, 4, 13, 144, 2576), (1, 4, 256, 2048, 6144),
+    (1, 8, 13, 144, 5392), (1, 8, 1, 144, 6160), (2, 4, 64, 4144, 2016), (2, 4, 1043, 592, 5984),
+    (2, 8, 64, 2080, 3760), (2, 8, 1038, 144, 5856), (2, 8, 64, 2064, 4128),
+    (3, 2, 8314, 144, 3984), (3, 4, 99, 4944, 5840), (3, 4, 65, 2704, 1712), (3, 8, 66, 1344, 3024),
+    (3, 8, 2063, 144, 5664), (3, 8, 65, 1312, 3088)]
+GROUPED_SPLIT = [  # tile, ways, experts, rows, mi, k, counts
+    (0, 2, 33, 1041, 144, 1936, "skew"), (0, 4, 3, 6, 144, 1472, "even"),
+    (0, 8, 3, 6, 160, 3056, "skew"), (0, 8, 3, 6, 144, 3088, "even"),
+    (1, 2, 37, 74, 144, 1792, "skew"), (1, 2, 80, 16, 656, 2960, "even"),
+    (1, 4, 3, 39, 160, 2592, "skew"), (1, 8, 3, 45, 144, 5760, "even"),
+    (1, 8, 3, 7, 144, 6208, "skew"), (2, 2, 34, 2176, 384, 6096, "even"),
+    (2, 4, 3, 192, 2016, 2448, "even"), (2, 8, 3, 192, 1024, 5776, "skew"),
+    (3, 2, 35, 1606, 144, 2656, "even"), (3, 4, 21, 972, 192, 3472, "skew"),
+    (3, 8, 11, 524, 144, 3056, "skew"), (3, 8, 9, 426, 144, 3152, "even")]
+
+
+def _ways(hip, experts, rows, n, k):
+    return hip.moe_fp8_swiglu_workspace_bytes(rows, experts, n, k) // (rows * n * 8)
+
+
+@pytest.mark.parametrize("tile,ways,m,n,k", DENSE_SPLIT)
+def test_dense_split(hip, tile, ways, m, n, k):
+    assert _ways(hip, 0, m, n, k) == ways
+    run_dense(hip, m, n, k, True)
+    if m * n * k < 3e8:
+        run_dense(hip, m, n, k, False)
+
+
+@pytest.mark.parametrize("tile,ways,experts,rows,mi,k,kind", GROUPED_SPLIT)
+def test_grouped_split(hip, tile, ways, experts, rows, mi, k, kind):
+    assert _ways(hip, experts, rows, mi, k) == ways
+    run_grouped(hip, experts, rows, mi, k, kind, True)
+    if rows * mi * k < 3e8:
+        run_grouped(hip, experts, rows, mi, k, kind, False)
+
+
+def test_grouped_split_leaves_uncovered_rows(hip):
+    """Rows before the first expert, of absent experts and behind the last one, on each tile."""
+    for tile, ways, experts, rows, mi, k, kind in GROUPED_SPLIT:
+        if rows * mi * k > 3e8 or rows < 30 or experts <= 3:
+            continue
+        off = _offsets(_counts(np.random.default_rng(rows), experts, rows - 9, kind)) + 4
+        run_grouped(hip, experts, rows, mi, k, kind, True, off)
