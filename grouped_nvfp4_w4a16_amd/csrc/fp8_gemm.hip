@@ -42,6 +42,8 @@
 //     32768 slots over 256 experts, (2048 + 2048) x 6144: 2026-2146 us, 770-814 TFLOP/s.
 //   - One token: the chain of a launch, the first loads and the steps of one tile, 5.7 us of
 //     kernel at 1 x 6144 x 2048.
+//   - The SwiGLU kernels of 256 x 128 and 256 x 192 spill 2 and 11 VGPRs (dense), 12 and 24
+//     (grouped), all outside their K loops.
 #include <mutex>
 #include <type_traits>
 
@@ -428,7 +430,8 @@ struct Share {
   }
 };
 
-// The item's rows as buffer resources: from the tile's first row, or (gathered) from row 0.
+// The item's rows as buffer resources: from the tile's first row, or (gathered) from row 0. A
+// gathered item loads its indices one row instruction after the other, each waited for.
 struct Rows {
   __amdgpu_buffer_rsrc_t codes, scales;
   const int32_t *gather;  // of the tile's first row, or NULL
@@ -454,7 +457,11 @@ struct Rows {
 // The tile's weight scales for all of K, sb[blk][kb_pad] in LDS, zeros past K and past the
 // last block row; blk: the gate's and the up's block (SwiGLU), or consecutive blocks. The
 // loads are issued with the item's other small loads, before the stages', and stored after
-// the stages' are on their way, so that no wait for them drains the stages.
+// the stages' are on their way. As compiled, the wait for them leaves the stages in flight in
+// the dense 32 x 16 and 256 x 128 kernels and the dense SwiGLU ones up to 128 rows. The others
+// wait for both stages once per item: the grouped ones, whose scale pointers come from memory
+// (flat loads, which count as LDS loads too), the dense 128 x 32 and 128 x 64 ones (before
+// their loop) and the 256 x 192 ones (spilled LDS addresses are reloaded there).
 template <int kNBlocks, int kThreads, bool kSwiglu>
 struct WeightScales {
   static constexpr int kPer = (kNBlocks * (kMaxK / kFp8Block + 8) + kThreads - 1) / kThreads;
