@@ -189,17 +189,23 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream):
-    """The handle of the given stream or of the current one (torch's internal query, where there
-    is one, makes no Stream object: 0.4 us, 2.7 with one)."""
+def _current_stream(device):
+    """The handle of a device's current stream, by torch's internal query where there is one: it
+    makes no Stream object (0.14 us, 1.1 to 2.5 with one)."""
     import torch
 
-    if stream is not None:
-        return stream.cuda_stream
-    query = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if query is None:
-        return torch.cuda.current_stream().cuda_stream
-    return query(torch.cuda.current_device())
+    try:
+        return torch._C._cuda_getCurrentRawStream(device)
+    except AttributeError:
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _stream(stream):
+    import torch
+
+    if stream is None:
+        return _current_stream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _want(t, dtype, name):
@@ -669,10 +675,10 @@ def _fp8_matrix(t, name):
     return stride[0]
 
 
-def _row_stride(ld, shape):
-    """The leading dimension to pass for a matrix of this shape: of a single row the stride says
-    nothing, its width (up to a multiple of 16) stands for it."""
-    return ld if shape[0] > 1 else (shape[1] + 15) & -16
+def _one_row(cols):
+    """The leading dimension to pass for a single row: its stride says nothing, its width (up to
+    a multiple of 16) stands for it."""
+    return (cols + 15) & -16
 
 
 def _scale_matrix(t, rows, cols, name, contiguous=False):
@@ -693,25 +699,29 @@ def _fp8_blocks(n):
     return -(-n // FP8_BLOCK)
 
 
-def _fits_int32(*sizes):
-    """Raises unless the library's 32-bit sizes hold these (ctypes would cut them)."""
-    for n in sizes:
-        if not -0x80000000 <= n <= 0x7FFFFFFF:
-            raise ValueError(f"{n} is no 32-bit size")
+_INT32_MAX = 0x7FFFFFFF
 
 
-def _same_device(stream, *tensors):
-    """Raises unless the stream and every tensor belong to the current device (the launch is
-    prepared for it and goes there)."""
+def _no_int32(*sizes):
+    """Raises for sizes of which one is past the library's 32 bits (ctypes would cut it)."""
+    raise ValueError(f"sizes {sizes}: one is no 32-bit size")
+
+
+def _launch_stream(stream, *tensors):
+    """The handle of the stream a call goes to, the given one or the current one. Raises unless it
+    and every tensor belong to the current device (the launch is prepared for it)."""
     import torch
 
     dev = torch.cuda.current_device()
-    at = dev if stream is None else getattr(stream, "device_index", dev)
-    if at != dev:
-        raise ValueError(f"the stream belongs to cuda:{at}, the current device is cuda:{dev}")
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor lies on {t.device}, the current device is cuda:{dev}")
+    if stream is None:
+        return _current_stream(dev)
+    at = getattr(stream, "device_index", dev)
+    if at != dev:
+        raise ValueError(f"the stream belongs to cuda:{at}, the current device is cuda:{dev}")
+    return stream.cuda_stream
 
 
 def moe_quant_fp8(x, q, scale, stream=None) -> None:
@@ -722,14 +732,16 @@ def moe_quant_fp8(x, q, scale, stream=None) -> None:
     rows, cols = x.shape
     if q.shape != x.shape:
         raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
-    _fits_int32(rows, cols)
-    ld_x, ld_q = _row_stride(ld_x, x.shape), _row_stride(ld_q, x.shape)
+    if rows > _INT32_MAX or cols > _INT32_MAX:
+        _no_int32(rows, cols)
+    if rows <= 1:
+        ld_x = ld_q = _one_row(cols)
     ld_s = _scale_matrix(scale, rows, _fp8_blocks(cols), "scale")
-    _same_device(stream, x, q, scale)
+    handle = _launch_stream(stream, x, q, scale)
     if cols == 0:
         return
     _check("moe_quant_fp8", load().moe_quant_fp8(
-        _p(x), ld_x, _p(q), ld_q, _p(scale), ld_s, rows, cols, _stream(stream)))
+        _p(x), ld_x, _p(q), ld_q, _p(scale), ld_s, rows, cols, handle))
 
 
 def moe_dense_gemm_fp8(a, a_scale, b, b_scale, c, stream=None) -> None:
@@ -743,15 +755,17 @@ def moe_dense_gemm_fp8(a, a_scale, b, b_scale, c, stream=None) -> None:
     if kw != k or c.shape != (m, n):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, "
                          f"c {tuple(c.shape)}")
-    _fits_int32(m, n, k)
-    lda, ldc = _row_stride(lda, (m, k)), _row_stride(ldc, (m, n))
+    if m > _INT32_MAX or n > _INT32_MAX or k > _INT32_MAX:
+        _no_int32(m, n, k)
+    if m <= 1:
+        lda, ldc = _one_row(k), _one_row(n)
     kb = _fp8_blocks(k)
     ld_as = _scale_matrix(a_scale, m, kb, "a_scale")
     _scale_matrix(b_scale, _fp8_blocks(n), kb, "b_scale", contiguous=True)
-    _same_device(stream, a, a_scale, b, b_scale, c)
+    handle = _launch_stream(stream, a, a_scale, b, b_scale, c)
     _check("moe_dense_gemm_fp8", load().moe_dense_gemm_fp8(
         _p(a), lda, _p(a_scale), ld_as, _p(b), ldb, _p(b_scale), _p(c), ldc, m, n, k,
-        _stream(stream)))
+        handle))
 
 
 def moe_fp8_swiglu_workspace_bytes(rows: int, num_experts: int, width: int, k: int) -> int:
@@ -759,7 +773,9 @@ def moe_fp8_swiglu_workspace_bytes(rows: int, num_experts: int, width: int, k: i
     ``num_experts`` 0, moe_dense_gate_up_swiglu_fp8 (``width`` = inter) splits these sizes
     with; 0 where they are not split."""
     rows, num_experts, width, k = int(rows), int(num_experts), int(width), int(k)
-    _fits_int32(rows, num_experts, width, k)
+    sizes = (rows, num_experts, width, k)
+    if max(sizes) > _INT32_MAX or min(sizes) < -_INT32_MAX:
+        _no_int32(*sizes)
     return int(load().moe_fp8_swiglu_workspace_bytes(rows, num_experts, width, k))
 
 
@@ -770,7 +786,6 @@ def _swiglu_workspace(ws, rows, num_experts, width, k, device, stream):
 
     if ws is not None:
         wp, wb = _workspace(ws)
-        _same_device(stream, ws)
         return ws, wp, wb
     need = load().moe_fp8_swiglu_workspace_bytes(rows, num_experts, width, k)
     if need == 0:
@@ -799,40 +814,47 @@ def moe_dense_gate_up_swiglu_fp8(a, a_scale, gate_w, gate_scale, up_w, up_scale,
     if gate_w.shape[1] != k or tuple(act.shape) != (m, inter):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, gate_w {tuple(gate_w.shape)}, "
                          f"act {tuple(act.shape)}")
-    _fits_int32(m, inter, k)
-    lda, ld_act = _row_stride(lda, (m, k)), _row_stride(ld_act, (m, inter))
+    if m > _INT32_MAX or inter > _INT32_MAX or k > _INT32_MAX:
+        _no_int32(m, inter, k)
+    if m <= 1:
+        lda, ld_act = _one_row(k), _one_row(inter)
     kb, ib = _fp8_blocks(k), _fp8_blocks(inter)
     ld_as = _scale_matrix(a_scale, m, kb, "a_scale")
     _scale_matrix(gate_scale, ib, kb, "gate_scale", contiguous=True)
     _scale_matrix(up_scale, ib, kb, "up_scale", contiguous=True)
     ld_os = _scale_matrix(act_scale, m, ib, "act_scale")
-    _same_device(stream, a, a_scale, gate_w, gate_scale, up_w, up_scale, act, act_scale)
+    handle = _launch_stream(stream, a, a_scale, gate_w, gate_scale, up_w, up_scale, act, act_scale,
+                            workspace)
     ws, wp, wb = _swiglu_workspace(workspace, m, 0, inter, k, a.device, stream)
     _check("moe_dense_gate_up_swiglu_fp8", load().moe_dense_gate_up_swiglu_fp8(
         _p(a), lda, _p(a_scale), ld_as, _p(gate_w), _p(gate_scale), _p(up_w), _p(up_scale), ldw,
         _p(act), ld_act, _p(act_scale), ld_os, m, inter, k, float(limit), wp, wb,
-        _stream(stream)))
+        handle))
 
 
 def _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows, out_rows):
-    """Checks the row side of a grouped FP8 call; (lda, ld_a_scale, rows)."""
+    """Checks the row side of a grouped FP8 call; (lda, ld_a_scale, a's rows, rows)."""
     import torch
 
-    lda = _row_stride(_fp8_matrix(a, "a"), a.shape)
+    lda = _fp8_matrix(a, "a")
+    a_rows, cols = a.shape
+    if a_rows <= 1:
+        lda = _one_row(cols)
     _want(expert_offsets, torch.int32, "expert_offsets")
     _want(a_gather, torch.int32, "a_gather")
     if expert_offsets.numel() < table.num_experts + 1 or not expert_offsets.is_contiguous():
         raise ValueError("expert_offsets: needs num_experts + 1 contiguous elements")
     rows = out_rows if max_rows is None else max_rows
-    _fits_int32(rows, a.shape[0], table.n, table.k)
+    if a_rows > _INT32_MAX or rows > _INT32_MAX or rows < -_INT32_MAX or table.n > _INT32_MAX:
+        _no_int32(a_rows, rows, table.n)
     if rows > out_rows or (a_gather is not None and
                            (a_gather.numel() < rows or not a_gather.is_contiguous())):
         raise ValueError("max_rows exceeds the output or a_gather")
-    if a_gather is None and rows > a.shape[0]:
+    if a_gather is None and rows > a_rows:
         raise ValueError("without a_gather, a needs max_rows rows")
-    if a.shape[1] < table.k:
+    if cols < table.k:
         raise ValueError("a too narrow for the table's k")
-    return lda, _scale_matrix(a_scale, a.shape[0], _fp8_blocks(table.k), "a_scale"), rows
+    return lda, _scale_matrix(a_scale, a_rows, _fp8_blocks(table.k), "a_scale"), a_rows, rows
 
 
 def moe_w8a8_grouped_gemm(a, a_scale, table: "Fp8ExpertTable", expert_offsets, c, a_gather=None,
@@ -840,18 +862,20 @@ def moe_w8a8_grouped_gemm(a, a_scale, table: "Fp8ExpertTable", expert_offsets, c
     """``c[s] = (a * a_scale)[g(s)] @ W_e^T`` in BF16 for every sorted row s of every present
     expert e of an ``Fp8ExpertTable``; see the header."""
     c, ldc = _bf16_matrix(c, "c")
-    lda, ld_as, rows = _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows,
-                                  c.shape[0])
+    out_rows, out_cols = c.shape
+    lda, ld_as, a_rows, rows = _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows,
+                                          out_rows)
     if table.gate_up:
         raise ValueError("a gate_up table goes to moe_w8a8_grouped_gemm_swiglu")
-    if c.shape[1] < table.n:
+    if out_cols < table.n:
         raise ValueError("c too narrow for the table's n")
-    ldc = _row_stride(ldc, c.shape)
-    _same_device(stream, a, a_scale, expert_offsets, c, a_gather, table.weight_ptrs)
+    if out_rows <= 1:
+        ldc = _one_row(out_cols)
+    handle = _launch_stream(stream, a, a_scale, expert_offsets, c, a_gather, table.weight_ptrs)
     _check("moe_w8a8_grouped_gemm", load().moe_w8a8_grouped_gemm(
-        _p(a), lda, _p(a_scale), ld_as, a.shape[0], _p(a_gather), _p(table.weight_ptrs),
+        _p(a), lda, _p(a_scale), ld_as, a_rows, _p(a_gather), _p(table.weight_ptrs),
         _p(table.scale_ptrs), _p(expert_offsets), table.num_experts, _p(c), ldc, rows, table.n,
-        table.k, _stream(stream)))
+        table.k, handle))
 
 
 def moe_w8a8_grouped_gemm_swiglu(a, a_scale, table: "Fp8ExpertTable", expert_offsets, act,
@@ -863,22 +887,25 @@ def moe_w8a8_grouped_gemm_swiglu(a, a_scale, table: "Fp8ExpertTable", expert_off
     ``act_scale [rows, ceil(mi / 128)]``. ``workspace`` as for moe_dense_gate_up_swiglu_fp8
     (moe_fp8_swiglu_workspace_bytes(rows, num_experts, mi, k) bytes)."""
     ld_act = _fp8_matrix(act, "act")
-    lda, ld_as, rows = _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows,
-                                  act.shape[0])
+    out_rows, out_cols = act.shape
+    lda, ld_as, a_rows, rows = _w8a8_rows(a, a_scale, table, expert_offsets, a_gather, max_rows,
+                                          out_rows)
     if not table.gate_up:
         raise ValueError("the table was not made with gate_up=True")
     mi = table.n // 2
-    if act.shape[1] < mi:
+    if out_cols < mi:
         raise ValueError("act too narrow for the table's n / 2")
-    ld_act = _row_stride(ld_act, act.shape)
+    if out_rows <= 1:
+        ld_act = _one_row(out_cols)
     ld_os = _scale_matrix(act_scale, rows, _fp8_blocks(mi), "act_scale")
-    _same_device(stream, a, a_scale, expert_offsets, act, act_scale, a_gather, table.weight_ptrs)
+    handle = _launch_stream(stream, a, a_scale, expert_offsets, act, act_scale, a_gather,
+                            table.weight_ptrs, workspace)
     ws, wp, wb = _swiglu_workspace(workspace, rows, table.num_experts, mi, table.k, a.device,
                                    stream)
     _check("moe_w8a8_grouped_gemm_swiglu", load().moe_w8a8_grouped_gemm_swiglu(
-        _p(a), lda, _p(a_scale), ld_as, a.shape[0], _p(a_gather), _p(table.weight_ptrs),
+        _p(a), lda, _p(a_scale), ld_as, a_rows, _p(a_gather), _p(table.weight_ptrs),
         _p(table.scale_ptrs), _p(expert_offsets), table.num_experts, _p(act), ld_act,
-        _p(act_scale), ld_os, rows, mi, table.k, float(limit), wp, wb, _stream(stream)))
+        _p(act_scale), ld_os, rows, mi, table.k, float(limit), wp, wb, handle))
 
 
 # ----------------------------------------------------------------------------- helpers
@@ -1290,7 +1317,7 @@ def moe_layer_fp8(x, topk_ids, topk_weights, gate_up: Fp8ExpertTable, down: Fp8E
         raise ValueError("the workspace was made for other sizes")
     if tuple(x.shape) != (rows, hidden) or tuple(out.shape) != (rows, hidden):
         raise ValueError(f"x and out must be [{rows}, {hidden}]")
-    _same_device(stream, x, topk_ids, topk_weights, out, ws.x)  # before the first launch
+    _launch_stream(stream, x, topk_ids, topk_weights, out, ws.x)  # before the first launch
     s = rows * top_k
     moe_align(topk_ids, gate_up.num_experts, ws.sorted_token_ids, ws.sorted_expert_ids,
               ws.expert_offsets, ws.token_to_perm, None, None, stream,

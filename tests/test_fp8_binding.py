@@ -245,7 +245,7 @@ def test_the_layer_holds_its_split_workspaces(monkeypatch):
 def test_the_current_stream_without_torchs_short_cut(lib, monkeypatch):
     """torch's internal query is a short cut: without it the public one serves."""
     monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream(0, 0x99))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(0, 0x99))
     for name, call in CALLS.items():
         call()
         assert lib.calls[-1][0] == name and lib.calls[-1][1][-1] == 0x99
