@@ -37,29 +37,31 @@ struct Fp8Plan {
 // width 160 x K 3728: 35.6 us, 26.3 with three stages of 64 rows). A
 // split adds a launch (6 with its wait) and writes and reads its sums, at 2.5 and 4 TB/s. HBM
 // bounds all of it (the experts' weights at 6 TB/s); a tenth of the estimate stands for what
-// does not run beside that. Over 400 random sizes the choice is 1.2 to 2.4 % slower than the
-// best (geometric mean; dense 1.2, dense SwiGLU 1.3, grouped SwiGLU 2.2, grouped 2.4).
+// does not run beside that. Over the 400 random sizes it was fitted to, the choice is 1.2 to 2.4 %
+// slower than the best (geometric mean); over 400 fresh ones 1.4 % (dense), 2.3 (dense SwiGLU),
+// 2.4 (grouped) and 4.1 (grouped SwiGLU), 1.32 times at worst (grouped, 148 slots over 88
+// experts, 288 x 1616: 14.2 us on 32 x 16, 10.7 on 128 x 32).
 //
-// Both sides, measured in us, the one taken marked (where it is not the least, it loses 0.3 to
-// 7 %):
+// Both sides, measured in us (ranges: two machines), the one taken marked (where it is not the
+// least, it loses up to 7 %; one matrix of few rows is bound by the host in these calls):
 //   plain, N 6144 x K 2048            32 x 16   128 x 32   128 x 64   256 x 128
-//     1 row                              9.3*       10.7        9.9        14.4
-//     64 rows                            9.1         9.7*      12.7        15.0
-//     256 rows                          25.6        13.1       13.5*       19.5
-//     1024 rows                         90.8        35.5       28.3        23.1*
-//     4096 rows                          348         128       95.3        72.0*
-//     256 experts, 8 rows each           691         557*       562         561
-//     256 experts, 32 rows each         1278         648        605         607*
-//     256 experts, 128 rows each        3985        1518       1227         896*
+//     1 row                         9.3-11.1*  10.3-10.7   9.9-10.4  14.4-14.8
+//     64 rows                        9.1-10.4  9.7-10.7*  12.7-13.2  15.0-15.4
+//     256 rows                           26.2  13.1-13.7  13.5-13.7*      20.3
+//     1024 rows                          91.4       35.5  26.6-28.3  23.1-23.4*
+//     4096 rows                           352        130  89.8-95.3  68.7-72.0*
+//     256 experts, 8 rows each            691   549-557*   552-562    560-561
+//     256 experts, 32 rows each          1321   648-704    605-638    607-620*
+//     256 experts, 128 rows each         4260       1518       1227   896-904*
 //   SwiGLU, width 2048 x K 6144       256 x 32   256 x 64   256 x 128   256 x 192
-//     256 experts, 8 rows each     1064-1105  1073-1080*         -           -
-//     256 experts, 32 rows each         1365        1183*         -           -
-//     256 experts, 128 rows each           -        2858        2490        2026*
-//     4096 rows                            -         279         194*        275
+//     256 experts, 8 rows each     1064-1105  1040-1080*       1126        1114
+//     256 experts, 32 rows each    1365-1433  1183-1198*       1210        1232
+//     256 experts, 128 rows each        3494   2712-2858  2362-2490  2026-2069*
+//     4096 rows                          311    279-284    194-197*    275-278
 //   (most of those experts of 128 rows pass 128 by a few: they would take two 128-row tiles)
 //   split of K, the same width            1          2          4           8
-//     8 rows, 256 x 32                  38.9       23.8       16.5        14.0*
-//     256 rows, 256 x 64                66.5       41.7       30.6*       36.7
+//     8 rows, 256 x 32                  38.9       23.8       16.5   14.0-14.5*
+//     256 rows, 256 x 64                66.5       41.7  29.8-30.6*       36.7
 template <bool kSwiglu>
 Fp8Plan fp8_plan(int64_t rows, int64_t experts, int64_t n, int64_t k, bool split, int cus) {
   const double used = experts > 0 ? static_cast<double>(experts < rows ? experts : rows) : 1.0;
