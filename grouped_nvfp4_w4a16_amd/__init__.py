@@ -1317,7 +1317,9 @@ def moe_layer_fp8(x, topk_ids, topk_weights, gate_up: Fp8ExpertTable, down: Fp8E
         raise ValueError("the workspace was made for other sizes")
     if tuple(x.shape) != (rows, hidden) or tuple(out.shape) != (rows, hidden):
         raise ValueError(f"x and out must be [{rows}, {hidden}]")
-    _launch_stream(stream, x, topk_ids, topk_weights, out, ws.x)  # before the first launch
+    term = shared.partials if isinstance(shared, SharedPartials) else getattr(shared, "out", shared)
+    _launch_stream(stream, x, topk_ids, topk_weights, out, ws.x, gate_up.weight_ptrs,
+                   down.weight_ptrs, term)  # before the first launch
     s = rows * top_k
     moe_align(topk_ids, gate_up.num_experts, ws.sorted_token_ids, ws.sorted_expert_ids,
               ws.expert_offsets, ws.token_to_perm, None, None, stream,

@@ -142,14 +142,30 @@ class Workspace:
         self.x = Tensor((4, 256), F8, device=device)
 
 
-@pytest.mark.parametrize("case", ["stream", "x", "workspace"])
+class Shared:
+    """A shared expert's output buffer."""
+
+    def __init__(self, device):
+        self.out = Tensor((4, 256), BF16, device=device)
+
+
+class Partials(pkg.SharedPartials):
+    def __init__(self, device):
+        self.partials, self.ways = Tensor((2, 4, 256), F32, device=device), 2
+
+
+@pytest.mark.parametrize("case", ["stream", "x", "workspace", "gate_up", "down", "shared term",
+                                  "shared partials", "shared expert"])
 def test_a_layer_on_another_device_launches_nothing(lib, case):
     at = {case: 1}
     ids, w = Tensor((4, 2), I32), Tensor((4, 2), F32)
+    shared = {"shared term": Tensor((4, 256), BF16, device=1), "shared partials": Partials(1),
+              "shared expert": Shared(1)}.get(case)
     with pytest.raises(ValueError, match="cuda:1"):
         pkg.moe_layer_fp8(Tensor((4, 256), BF16, device=at.get("x", 0)), ids, w,
-                          Table(3, 288, 256, True), Table(3, 256, 144), 7.0,
-                          Workspace(at.get("workspace", 0)), Tensor((4, 256), BF16),
+                          Table(3, 288, 256, True, at.get("gate_up", 0)),
+                          Table(3, 256, 144, device=at.get("down", 0)), 7.0,
+                          Workspace(at.get("workspace", 0)), Tensor((4, 256), BF16), shared,
                           stream=Stream(at.get("stream", 0)))
     assert lib.calls == []
 
