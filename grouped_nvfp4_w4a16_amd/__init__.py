@@ -1261,8 +1261,8 @@ class Fp8Workspace:
         self.act = torch.empty(s, moe_intermediate, **f8)
         self.act_scale = torch.empty(s, _fp8_blocks(moe_intermediate), **f32)
         self.expert_out = torch.empty(s, hidden, dtype=torch.bfloat16, device=device)
-        self.split = _split_workspace(range(top_k, s + 1, top_k), num_experts, moe_intermediate,
-                                      hidden, device)
+        self.split = _split_workspace((r * top_k for r in range(1, max_rows + 1)), num_experts,
+                                      moe_intermediate, hidden, device)
 
 
 class SharedExpertFp8:

@@ -252,6 +252,7 @@ def test_the_layer_holds_its_split_workspaces(monkeypatch):
     assert pkg.Fp8Workspace(6, 2, 3, 256, 144, device="cpu").split.numel() == 256
     assert pkg.Fp8Workspace(6, 3, 3, 256, 144, device="cpu").split.numel() == 512
     assert pkg.Fp8Workspace(2, 2, 3, 256, 144, device="cpu").split is None
+    assert pkg.Fp8Workspace(2, 0, 3, 256, 144, device="cpu").split is None
     w, s = torch.empty(144, 256), torch.empty(2, 2)
     for rows, need in ((9, 512), (3, 512), (1, None)):
         sh = pkg.SharedExpertFp8(w, s, w, s, w.t().contiguous(), s, rows)
