@@ -80,3 +80,55 @@ def test_a_layer_call_allocates_nothing(hip, rows):
         assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
         outs.append(out)
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("own_workspace", [False, True])
+def test_split_products_captured_and_replayed(hip, own_workspace):
+    """Split-K SwiGLU calls in a graph, dense and grouped, through the caller's workspace and the
+    call's own (from the graph's pool); every replay on other inputs, with eager calls of the
+    same sizes between the replays, against the eager result."""
+    torch.manual_seed(3)
+    m, n, k, experts = 12, 144, 2064, 4
+    need = max(hip.moe_fp8_swiglu_workspace_bytes(m, e, n, k) for e in (0, experts))
+    assert min(hip.moe_fp8_swiglu_workspace_bytes(m, e, n, k) for e in (0, experts)) > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if own_workspace else None
+
+    def weight(rows, blocks):
+        w = torch.randint(0, 120, (rows, k), dtype=torch.uint8, device="cuda")
+        return w, torch.rand(blocks, 17, device="cuda") / 1000
+
+    gate, up = weight(n, 2), weight(n, 2)
+    table = hip.Fp8ExpertTable(*zip(*[weight(2 * n, 4) for _ in range(experts)]), 2 * n, k,
+                               gate_up=True)
+    off = torch.tensor([0, 5, 5, 9, 12], dtype=torch.int32, device="cuda")
+    a = torch.empty((m, k), dtype=torch.uint8, device="cuda")
+    sa = torch.empty((m, 17), device="cuda")
+
+    def outputs():
+        return [(torch.zeros((m, n), dtype=torch.uint8, device="cuda"),
+                 torch.zeros((m, 2), device="cuda")) for _ in range(2)]
+
+    def calls(out, work):
+        hip.moe_dense_gate_up_swiglu_fp8(a, sa, *gate, *up, *out[0], 7.0, workspace=work)
+        hip.moe_w8a8_grouped_gemm_swiglu(a, sa, table, off, *out[1], 7.0, workspace=work)
+
+    def fill():
+        a.copy_(torch.randint(0, 120, (m, k), dtype=torch.uint8, device="cuda"))
+        sa.copy_(torch.rand(m, 17, device="cuda"))
+
+    fill()
+    captured, eager = outputs(), outputs()
+    calls(captured, ws)  # attributes are set before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls(captured, ws)
+    for _ in range(4):
+        fill()
+        graph.replay()
+        torch.cuda.synchronize()
+        calls(eager, None)
+        torch.cuda.synchronize()
+        for got, want in zip(captured, eager):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            assert bool(want[0].any())
