@@ -19,13 +19,20 @@ Calls (same names as the C ABI):
 - ``moe_quant_fp8``, ``moe_w8a8_grouped_gemm``, ``moe_w8a8_grouped_gemm_swiglu``,
   ``moe_dense_gemm_fp8``, ``moe_dense_gate_up_swiglu_fp8``: the layer and the shared expert on
   E4M3 weights and activations with one FP32 scale per block of 128.
+- ``moe_rmsnorm_bf16``, ``moe_rmsnorm_fp8``, ``moe_rmsnorm_int8``: the residual's addition and
+  the root-mean-square norm before the layer, with its rows in BF16 and quantised;
+  ``moe_quant_int8``: rows to INT8.
+- ``moe_dense_gemm_int8``, ``moe_dense_gate_up_swiglu_int8``: the shared expert's products in
+  INT8 with one FP32 scale per token and per output channel.
 
 Helpers: ``ExpertTable`` (device pointer table of per-expert NVFP4 weights),
 ``Workspace`` (every buffer of one layer call, allocated once), ``SharedExpert`` (the
 shared expert's weights and buffers), ``moe_layer`` (the calls of one routed layer in
 order), ``DecodeWorkspace`` and ``moe_layer_decode`` (the same layer for a few rows through
 the union path), and their FP8 counterparts ``Fp8ExpertTable``, ``Fp8Workspace``,
-``SharedExpertFp8`` and ``moe_layer_fp8``.
+``SharedExpertFp8`` and ``moe_layer_fp8``; ``SharedExpertInt8`` (the shared expert in INT8);
+``FewWorkspace``, ``moe_layer_few`` and ``moe_layer_few_from_logits`` (a whole layer of a few
+tokens in two kernels, moe_w4a16_layer_few).
 """
 
 from __future__ import annotations
@@ -46,6 +53,9 @@ __all__ = [
     "moe_quant_fp8", "moe_dense_gemm_fp8", "moe_dense_gate_up_swiglu_fp8",
     "moe_w8a8_grouped_gemm", "moe_w8a8_grouped_gemm_swiglu", "Fp8ExpertTable", "Fp8Workspace",
     "SharedExpertFp8", "moe_layer_fp8", "FP8_MAX_K", "moe_fp8_swiglu_workspace_bytes",
+    "moe_rmsnorm_bf16", "moe_rmsnorm_fp8", "moe_rmsnorm_int8", "moe_quant_int8",
+    "moe_dense_gemm_int8", "moe_dense_gate_up_swiglu_int8", "SharedExpertInt8", "INT8_MAX_K",
+    "moe_layer_few", "moe_layer_few_from_logits", "FewWorkspace", "FEW_MAX_ROWS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_w4a16.so")
@@ -61,7 +71,10 @@ EXPORTS = (
     "moe_align_zero", "moe_dense_splitk_ways", "moe_dense_gemm_bf16_partials",
     "moe_combine_partials", "moe_quant_fp8", "moe_dense_gemm_fp8",
     "moe_dense_gate_up_swiglu_fp8", "moe_w8a8_grouped_gemm", "moe_w8a8_grouped_gemm_swiglu",
-    "moe_fp8_swiglu_workspace_bytes",
+    "moe_fp8_swiglu_workspace_bytes", "moe_rmsnorm_bf16", "moe_rmsnorm_fp8",
+    "moe_rmsnorm_int8", "moe_quant_int8", "moe_dense_gemm_int8",
+    "moe_dense_gate_up_swiglu_int8", "moe_shared_expert_int8",
+    "moe_shared_expert_int8_workspace_bytes", "moe_w4a16_layer_few", "moe_few_workspace_bytes",
 )
 
 UNION_MAX_IDS = 1024  # MOE_UNION_MAX_IDS: rows * top_k of moe_row_union
@@ -70,6 +83,9 @@ UNION_GEMV_MAX_IDS = 512  # MOE_UNION_GEMV_MAX_IDS: rows * top_k of moe_w4a16_ge
 DENSE_NOALLOC_SCRATCH_BYTES = 32 << 20  # MOE_DENSE_NOALLOC_SCRATCH_BYTES
 FP8_MAX_K = 32768  # MOE_FP8_MAX_K
 FP8_BLOCK = 128  # values per scale
+INT8_MAX_K = 131056  # MOE_INT8_MAX_K
+FEW_MAX_ROWS = 16  # MOE_FEW_MAX_ROWS: rows of moe_layer_few
+FEW_MAX_IDS = 256  # MOE_FEW_MAX_IDS: its rows * top_k
 
 _LIB = None
 
@@ -132,6 +148,26 @@ _SIGNATURES = {
     "moe_w8a8_grouped_gemm_swiglu": (
         [_vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _i64, _i32, _i32,
          _i32, _f32, _vp, _i64, _vp], ctypes.c_int),
+    "moe_rmsnorm_bf16": ([_vp, _i64, _vp, _i64, _vp, _f32, _vp, _i64, _vp, _i64, _i32, _i32,
+                          _vp], ctypes.c_int),
+    "moe_rmsnorm_fp8": ([_vp, _i64, _vp, _i64, _vp, _f32, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                         _i64, _i32, _i32, _vp], ctypes.c_int),
+    "moe_rmsnorm_int8": ([_vp, _i64, _vp, _i64, _vp, _f32, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                          _i32, _i32, _vp], ctypes.c_int),
+    "moe_quant_int8": ([_vp, _i64, _vp, _i64, _vp, _i32, _i32, _vp], ctypes.c_int),
+    "moe_dense_gemm_int8": ([_vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _vp],
+                            ctypes.c_int),
+    "moe_dense_gate_up_swiglu_int8": (
+        [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _f32, _vp],
+        ctypes.c_int),
+    "moe_shared_expert_int8": (
+        [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32,
+         _f32, _vp, _i64, _vp], ctypes.c_int),
+    "moe_shared_expert_int8_workspace_bytes": ([_i32, _i32], _i64),
+    "moe_w4a16_layer_few": (
+        [_vp, _i64, _vp, _i64, _vp, _f32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp,
+         _i64, _vp, _i64, _i32, _i32, _i32, _i32, _f32, _vp, _i64, _vp], ctypes.c_int),
+    "moe_few_workspace_bytes": ([_i32, _i32, _i32], _i64),
 }
 
 
@@ -908,6 +944,176 @@ def moe_w8a8_grouped_gemm_swiglu(a, a_scale, table: "Fp8ExpertTable", expert_off
         _p(act_scale), ld_os, rows, mi, table.k, float(limit), wp, wb, handle))
 
 
+def _like_rows(t, rows, cols, name):
+    """(tensor, leading dimension) of an optional BF16 [rows, cols] device tensor."""
+    if t is None:
+        return None, 0
+    t, ld = _bf16_matrix(t, name)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: expected [{rows}, {cols}], got {tuple(t.shape)}")
+    return t, _one_row(cols) if rows <= 1 else ld
+
+
+def _norm_rows(x, weight, residual, h, y):
+    """Checks the BF16 side of a norm; (rows, cols, leading dimensions of x, residual, h, y)."""
+    import torch
+
+    x, ld_x = _bf16_matrix(x, "x")
+    rows, cols = x.shape
+    if rows > _INT32_MAX or cols > _INT32_MAX:
+        _no_int32(rows, cols)
+    if weight.dtype != torch.bfloat16 or weight.shape != (cols,) or not weight.is_contiguous():
+        raise ValueError(f"weight: expected {cols} contiguous BF16 values")
+    ld_r = _like_rows(residual, rows, cols, "residual")[1]
+    ld_h = _like_rows(h, rows, cols, "h")[1]
+    ld_y = _like_rows(y, rows, cols, "y")[1]
+    return rows, cols, _one_row(cols) if rows <= 1 else ld_x, ld_r, ld_h, ld_y
+
+
+def moe_rmsnorm_bf16(x, weight, y, eps: float = 1e-6, residual=None, h=None,
+                     stream=None) -> None:
+    """``h = bf16(x + residual)`` and ``y = bf16(h * weight / sqrt(mean(h^2) + eps))`` over BF16
+    ``[rows, cols]`` views; ``h`` (the new residual stream, where given) may be ``x`` or
+    ``residual``, ``y`` may be ``x``."""
+    rows, cols, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
+    if y is None:
+        raise TypeError("y: expected a BF16 tensor")
+    handle = _launch_stream(stream, x, weight, residual, h, y)
+    if cols == 0:
+        return
+    _check("moe_rmsnorm_bf16", load().moe_rmsnorm_bf16(
+        _p(x), ld_x, _p(residual), ld_r, _p(weight), float(eps), _p(h), ld_h, _p(y), ld_y, rows,
+        cols, handle))
+
+
+def moe_rmsnorm_fp8(x, weight, q, scale, eps: float = 1e-6, residual=None, h=None, y=None,
+                    stream=None) -> None:
+    """moe_rmsnorm_bf16 with its rows quantised, as moe_quant_fp8 does, from the unrounded norm:
+    E4M3 ``q [rows, cols]``, ``scale [rows, ceil(cols / 128)]``; ``y`` too where given."""
+    rows, cols, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
+    ld_q = _fp8_matrix(q, "q")
+    if q.shape != x.shape:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
+    if rows <= 1:
+        ld_q = _one_row(cols)
+    ld_s = _scale_matrix(scale, rows, _fp8_blocks(cols), "scale")
+    handle = _launch_stream(stream, x, weight, residual, h, y, q, scale)
+    if cols == 0:
+        return
+    _check("moe_rmsnorm_fp8", load().moe_rmsnorm_fp8(
+        _p(x), ld_x, _p(residual), ld_r, _p(weight), float(eps), _p(h), ld_h, _p(y), ld_y, _p(q),
+        ld_q, _p(scale), ld_s, rows, cols, handle))
+
+
+def _int8_matrix(t, name):
+    """Leading dimension of a row-major 2-D device tensor of INT8 codes."""
+    import torch
+
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name}: expected INT8 codes, got {t.dtype}")
+    stride = t.stride()
+    if len(stride) != 2 or stride[1] != 1 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a row-major 2-D device tensor")
+    return stride[0]
+
+
+def _scale_vector(t, n, name):
+    """Checks a contiguous float32 device vector of at least n scales."""
+    import torch
+
+    if t.dtype != torch.float32 or len(t.shape) != 1 or not t.is_cuda:
+        raise TypeError(f"{name}: expected a 1-D float32 device tensor")
+    if t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: needs {n} contiguous scales")
+
+
+def moe_rmsnorm_int8(x, weight, q, scale, eps: float = 1e-6, residual=None, h=None, y=None,
+                     stream=None) -> None:
+    """moe_rmsnorm_bf16 with its rows quantised, as moe_quant_int8 does, from the unrounded norm:
+    INT8 ``q [rows, cols]``, ``scale [rows]``; ``y`` too where given."""
+    rows, cols, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
+    ld_q = _int8_matrix(q, "q")
+    if q.shape != x.shape:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
+    if rows <= 1:
+        ld_q = _one_row(cols)
+    _scale_vector(scale, rows, "scale")
+    handle = _launch_stream(stream, x, weight, residual, h, y, q, scale)
+    if cols == 0:
+        return
+    _check("moe_rmsnorm_int8", load().moe_rmsnorm_int8(
+        _p(x), ld_x, _p(residual), ld_r, _p(weight), float(eps), _p(h), ld_h, _p(y), ld_y, _p(q),
+        ld_q, _p(scale), rows, cols, handle))
+
+
+def moe_quant_int8(x, q, scale, stream=None) -> None:
+    """Quantise BF16 rows ``x [rows, cols]`` to INT8 codes ``q [rows, cols]`` with one FP32 scale
+    per row, ``scale [rows]``; see the header."""
+    x, ld_x = _bf16_matrix(x, "x")
+    ld_q = _int8_matrix(q, "q")
+    rows, cols = x.shape
+    if q.shape != x.shape:
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
+    if rows > _INT32_MAX or cols > _INT32_MAX:
+        _no_int32(rows, cols)
+    if rows <= 1:
+        ld_x = ld_q = _one_row(cols)
+    _scale_vector(scale, rows, "scale")
+    handle = _launch_stream(stream, x, q, scale)
+    if cols == 0:
+        return
+    _check("moe_quant_int8", load().moe_quant_int8(
+        _p(x), ld_x, _p(q), ld_q, _p(scale), rows, cols, handle))
+
+
+def moe_dense_gemm_int8(a, a_scale, b, b_scale, c, stream=None) -> None:
+    """``c[m, n] = a[m, :] @ b[n, :] * a_scale[m] * b_scale[n]`` for INT8 ``a [M, K]`` and
+    ``b [N, K]`` with ``a_scale [M]`` and ``b_scale [N]``, BF16 ``c [M, N]``."""
+    lda, ldb = _int8_matrix(a, "a"), _int8_matrix(b, "b")
+    c, ldc = _bf16_matrix(c, "c")
+    m, k = a.shape
+    n, kw = b.shape
+    if kw != k or c.shape != (m, n):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, "
+                         f"c {tuple(c.shape)}")
+    if m > _INT32_MAX or n > _INT32_MAX or k > _INT32_MAX:
+        _no_int32(m, n, k)
+    if m <= 1:
+        lda, ldc = _one_row(k), _one_row(n)
+    _scale_vector(a_scale, m, "a_scale")
+    _scale_vector(b_scale, n, "b_scale")
+    handle = _launch_stream(stream, a, a_scale, b, b_scale, c)
+    _check("moe_dense_gemm_int8", load().moe_dense_gemm_int8(
+        _p(a), lda, _p(a_scale), _p(b), ldb, _p(b_scale), _p(c), ldc, m, n, k, handle))
+
+
+def moe_dense_gate_up_swiglu_int8(a, a_scale, gate_w, gate_scale, up_w, up_scale, act,
+                                  limit: float, stream=None) -> None:
+    """The shared expert's gate and up products (``gate_w``, ``up_w`` INT8 ``[I, K]``, same
+    strides, ``gate_scale``, ``up_scale [I]``) of INT8 rows ``a [M, K]`` with ``a_scale [M]``, and
+    the clamped SwiGLU: BF16 ``act [M, I]``."""
+    lda, ldw = _int8_matrix(a, "a"), _int8_matrix(gate_w, "gate_w")
+    act, ld_act = _bf16_matrix(act, "act")
+    if _int8_matrix(up_w, "up_w") != ldw or up_w.shape != gate_w.shape:
+        raise ValueError("gate_w and up_w must have the same shape and strides")
+    m, k = a.shape
+    inter = gate_w.shape[0]
+    if gate_w.shape[1] != k or act.shape != (m, inter):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, gate_w {tuple(gate_w.shape)}, "
+                         f"act {tuple(act.shape)}")
+    if m > _INT32_MAX or inter > _INT32_MAX or k > _INT32_MAX:
+        _no_int32(m, inter, k)
+    if m <= 1:
+        lda, ld_act = _one_row(k), _one_row(inter)
+    _scale_vector(a_scale, m, "a_scale")
+    _scale_vector(gate_scale, inter, "gate_scale")
+    _scale_vector(up_scale, inter, "up_scale")
+    handle = _launch_stream(stream, a, a_scale, gate_w, gate_scale, up_w, up_scale, act)
+    _check("moe_dense_gate_up_swiglu_int8", load().moe_dense_gate_up_swiglu_int8(
+        _p(a), lda, _p(a_scale), _p(gate_w), _p(gate_scale), _p(up_w), _p(up_scale), ldw, _p(act),
+        ld_act, m, inter, k, float(limit), handle))
+
+
 # ----------------------------------------------------------------------------- helpers
 
 class SharedExpert:
@@ -971,6 +1177,66 @@ class SharedExpert:
         # the workspace's partial tiles are read by the gate/up reduction before (stream
         # order) the down projection's partials overwrite them
         return moe_dense_gemm_bf16_partials(act, self.down_w, ws.view(torch.float32), stream)
+
+
+class SharedExpertInt8:
+    """The shared expert in INT8: ``gate_w``, ``up_w`` ``[I, H]`` and ``down_w`` ``[H, I]`` INT8
+    device tensors with one FP32 scale per output channel, plus its buffers for up to
+    ``max_rows`` rows. Calling it on quantised rows (``x [rows, H]``, ``x_scale [rows]``) runs
+    moe_shared_expert_int8 and returns the BF16 ``[rows, H]`` output view, a layer's ``shared``
+    term. Its calls must be ordered on one stream."""
+
+    def __init__(self, gate_w, gate_scale, up_w, up_scale, down_w, down_scale, max_rows: int):
+        import torch
+
+        inter, hidden = gate_w.shape
+        if tuple(up_w.shape) != (inter, hidden) or tuple(down_w.shape) != (hidden, inter):
+            raise ValueError("expected gate_w, up_w [I, H] and down_w [H, I]")
+        self.ld_w, self.ld_down = _int8_matrix(gate_w, "gate_w"), _int8_matrix(down_w, "down_w")
+        if _int8_matrix(up_w, "up_w") != self.ld_w:
+            raise ValueError("gate_w and up_w must have the same strides")
+        for t, n, name in ((gate_scale, inter, "gate_scale"), (up_scale, inter, "up_scale"),
+                           (down_scale, hidden, "down_scale")):
+            _scale_vector(t, n, name)
+        dev = gate_w.device
+        for t in (gate_scale, up_w, up_scale, down_w, down_scale):
+            if t.device != dev:
+                raise ValueError("the weights and scales lie on several devices")
+        self.gate, self.up, self.down = (gate_w, gate_scale), (up_w, up_scale), (down_w, down_scale)
+        self.inter, self.hidden = inter, hidden
+        self.x_q = torch.empty(max_rows, hidden, dtype=torch.int8, device=dev)
+        self.x_scale = torch.empty(max_rows, dtype=torch.float32, device=dev)
+        self.out = torch.empty(max_rows, hidden, dtype=torch.bfloat16, device=dev)
+        need = int(load().moe_shared_expert_int8_workspace_bytes(max_rows, inter))
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        self._weights = [_p(t) for t in (*self.gate, *self.up, *self.down)]
+
+    def _rows(self, x):
+        rows, hidden = x.shape
+        if rows > self.out.shape[0]:
+            raise ValueError(f"{rows} rows exceed the {self.out.shape[0]} the buffers hold")
+        if hidden != self.hidden:
+            raise ValueError(f"expected rows of {self.hidden} values, got {hidden}")
+        return rows
+
+    def __call__(self, x, x_scale, limit: float, stream=None):
+        rows = self._rows(x)
+        ldx = _int8_matrix(x, "x")
+        _scale_vector(x_scale, rows, "x_scale")
+        handle = _launch_stream(stream, x, x_scale, self.out)
+        gw, gs, uw, us, dw, ds = self._weights
+        _check("moe_shared_expert_int8", load().moe_shared_expert_int8(
+            _p(x), _one_row(self.hidden) if rows <= 1 else ldx, _p(x_scale), gw, gs, uw, us,
+            self.ld_w, dw, self.ld_down, ds, _p(self.out), self.hidden, rows, self.inter,
+            self.hidden, float(limit), _p(self.workspace), self.workspace.numel(), handle))
+        return self.out[:rows]
+
+    def for_combine(self, x, limit: float, stream=None):
+        """The combine's shared term for BF16 rows ``x``: quantises them, then __call__."""
+        rows = self._rows(x)
+        q, scale = self.x_q[:rows], self.x_scale[:rows]
+        moe_quant_int8(x, q, scale, stream)
+        return self(q, scale, limit, stream)
 
 
 class ExpertTable:
@@ -1062,9 +1328,9 @@ def moe_layer(x, topk_ids, topk_weights, gate_up: ExpertTable, down: ExpertTable
     GEMM writes every row the combine reads (each valid slot's row lies in its expert's
     segment), so the zeroing is skipped.
     ``shared`` is the combine's shared term: a ``[rows, H]`` BF16 tensor, a
-    ``SharedPartials``, or a ``SharedExpert``, which is then run over ``x`` after the routed
-    experts (its down projection's split-K reduction inside the combine when it runs in
-    the split-K form: same bits)."""
+    ``SharedPartials``, or a ``SharedExpert`` or ``SharedExpertInt8``, which is then run over
+    ``x`` after the routed experts (a ``SharedExpert``'s down projection's split-K reduction
+    inside the combine when it runs in the split-K form: same bits)."""
     _same_experts(gate_up, down)
     rows, top_k = topk_ids.shape
     s = rows * top_k
@@ -1083,7 +1349,7 @@ def moe_layer(x, topk_ids, topk_weights, gate_up: ExpertTable, down: ExpertTable
         swiglu_clamp(ws.gate_up[:s, :mi], ws.gate_up[:s, mi:2 * mi], ws.act[:s], limit, stream)
     moe_w4a16_grouped_gemm(ws.act, down, ws.expert_offsets, ws.expert_out, None, max_rows=s,
                            stream=stream, **active)
-    if isinstance(shared, SharedExpert):
+    if isinstance(shared, (SharedExpert, SharedExpertInt8)):
         shared = shared.for_combine(x, limit, stream)
     moe_combine(ws.expert_out[:s], ws.token_to_perm, topk_weights, out, shared, stream)
 
@@ -1156,9 +1422,107 @@ def moe_layer_decode(x, topk_ids, topk_weights, gate_up: ExpertTable, down: Expe
         swiglu_clamp(ws.gate_up[:t, :mi], ws.gate_up[:t, mi:2 * mi], ws.act[:t], limit, stream)
     moe_w4a16_gemv_union(ws.act, down, ws.u_eid, u_slot, ws.expert_out, rows, top_k,
                          a_per_slot=True, stream=stream)
-    if isinstance(shared, SharedExpert):
+    if isinstance(shared, (SharedExpert, SharedExpertInt8)):
         shared = shared.for_combine(x, limit, stream)
     moe_combine(ws.expert_out[:t], ws.slot_perm[:t], topk_weights, out, shared, stream)
+
+
+class FewWorkspace:
+    """The buffer of moe_layer_few calls of up to ``max_rows`` (<= 16) rows. Calls that share it
+    must be ordered on one stream."""
+
+    def __init__(self, max_rows: int, top_k: int, moe_intermediate: int, device="cuda"):
+        import torch
+
+        if not 1 <= max_rows <= FEW_MAX_ROWS or not 1 <= top_k <= FEW_MAX_IDS // max_rows:
+            raise ValueError("the few-token layer takes 1..16 rows and rows * top_k <= 256")
+        self.max_rows, self.top_k = max_rows, top_k
+        self.moe_intermediate = moe_intermediate
+        need = int(load().moe_few_workspace_bytes(max_rows, top_k, moe_intermediate))
+        self.buffer = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+
+
+def _layer_few(x, logits, bias, routed_scale, renormalize, topk_ids, topk_weights, top_k, gate_up,
+               down, limit, ws, out, shared, stream):
+    _same_experts(gate_up, down)
+    rows, hidden, mi = x.shape[0], gate_up.k, down.k
+    if gate_up.n != 2 * mi or down.n != hidden:
+        raise ValueError("expected a gate_up table [2 mi, H] and a down table [H, mi]")
+    if rows > ws.max_rows or top_k != ws.top_k or mi != ws.moe_intermediate:
+        raise ValueError("the workspace was made for other sizes")
+    x, ld_x = _bf16_matrix(x, "x")
+    out, ld_out = _bf16_matrix(out, "out")
+    if x.shape[1] != hidden or out.shape != x.shape:
+        raise ValueError(f"x and out must be [{rows}, {hidden}]")
+    if isinstance(shared, (SharedExpert, SharedExpertInt8)):
+        term = shared.out
+    else:
+        term = shared
+    handle = _launch_stream(stream, x, logits, bias, topk_ids, topk_weights, out, ws.buffer, term,
+                            gate_up.packed_ptrs, down.packed_ptrs)  # before the first launch
+    if isinstance(shared, (SharedExpert, SharedExpertInt8)):
+        shared = shared(x, limit, stream) if isinstance(shared, SharedExpert) else \
+            shared.for_combine(x, limit, stream)
+    ld_s = 0
+    if shared is not None:
+        shared, ld_s = _bf16_matrix(shared, "shared")
+        if shared.shape != x.shape:
+            raise ValueError(f"shared must be [{rows}, {hidden}]")
+    if rows <= 1:
+        ld_x = ld_out = ld_s = _one_row(hidden)
+    _check("moe_w4a16_layer_few", load().moe_w4a16_layer_few(
+        _p(x), ld_x, _p(logits), 0 if logits is None else max(logits.stride(0), logits.shape[1]),
+        _p(bias), float(routed_scale), 1 if renormalize else 0, _p(topk_ids), _p(topk_weights),
+        _p(gate_up.packed_ptrs), _p(gate_up.scale_ptrs), _p(gate_up.scale2), _p(down.packed_ptrs),
+        _p(down.scale_ptrs), _p(down.scale2), gate_up.num_experts, _p(shared), ld_s, _p(out),
+        ld_out, rows, top_k, hidden, mi, float(limit), _p(ws.buffer), ws.buffer.numel(), handle))
+
+
+def moe_layer_few(x, topk_ids, topk_weights, gate_up: ExpertTable, down: ExpertTable,
+                  limit: float, ws: FewWorkspace, out, shared=None, stream=None) -> None:
+    """The routed layer for 1..16 rows in two kernels: gate_up with the SwiGLU clamp over the
+    union of the rows' experts, then down, the weighted sum and the shared term. Weights are
+    decoded to FP16 exactly, ``scale2`` multiplies the FP32 sums, and only the SwiGLU's output
+    is rounded to BF16 on the way, so outputs are nearer to the formula than ``moe_layer`` and
+    ``moe_layer_decode``, and not the same bits. ``shared`` is a BF16 ``[rows, H]`` tensor, a
+    ``SharedExpert`` or a ``SharedExpertInt8`` (run over ``x`` first)."""
+    import torch
+
+    _want(topk_ids, torch.int32, "topk_ids")
+    _want(topk_weights, torch.float32, "topk_weights")
+    rows, top_k = topk_ids.shape
+    if not topk_ids.is_contiguous() or not topk_weights.is_contiguous() or \
+            topk_weights.shape != topk_ids.shape or x.shape[0] != rows:
+        raise ValueError("topk_ids and topk_weights must be contiguous [rows, top_k]")
+    _layer_few(x, None, None, 1.0, True, topk_ids, topk_weights, top_k, gate_up, down, limit, ws,
+               out, shared, stream)
+
+
+def moe_layer_few_from_logits(x, logits, top_k: int, gate_up: ExpertTable, down: ExpertTable,
+                              limit: float, ws: FewWorkspace, out, bias=None,
+                              routed_scale: float = 1.0, renormalize: bool = True, shared=None,
+                              stream=None, topk_ids=None, topk_weights=None) -> None:
+    """moe_layer_few from FP32 router logits ``[rows, E]``, the routing found inside the first
+    kernel as moe_router_topk finds it (above 512 experts, in a launch of its own). ``topk_ids``
+    int32 and ``topk_weights`` float32 ``[rows, top_k]`` receive it where given."""
+    import torch
+
+    if logits.dim() != 2 or logits.dtype != torch.float32 or not logits.is_cuda:
+        raise TypeError("logits: expected a 2-D float32 device tensor")
+    rows, n_exp = x.shape[0], gate_up.num_experts
+    if logits.shape != (rows, n_exp) or (n_exp > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits: expected [{rows}, {n_exp}], rows contiguous")
+    _want(topk_ids, torch.int32, "topk_ids")
+    _want(topk_weights, torch.float32, "topk_weights")
+    for t, name in ((topk_ids, "topk_ids"), (topk_weights, "topk_weights")):
+        if t is not None and (t.shape != (rows, top_k) or not t.is_contiguous()):
+            raise ValueError(f"{name}: expected a contiguous [{rows}, {top_k}] tensor")
+    if bias is not None:
+        _want(bias, torch.float32, "bias")
+        if bias.shape != (n_exp,) or not bias.is_contiguous():
+            raise ValueError(f"bias: expected {n_exp} contiguous entries")
+    _layer_few(x, logits, bias, routed_scale, renormalize, topk_ids, topk_weights, int(top_k),
+               gate_up, down, limit, ws, out, shared, stream)
 
 
 # ------------------------------------------------------------------------- FP8 helpers
@@ -1306,7 +1670,7 @@ def moe_layer_fp8(x, topk_ids, topk_weights, gate_up: Fp8ExpertTable, down: Fp8E
     gate_up with the SwiGLU clamp and the quantisation of its output -> grouped down ->
     indexed combine into the BF16 ``out``. ``shared`` is the combine's shared term: a BF16
     ``[rows, H]`` tensor, a ``SharedPartials``, a ``SharedExpertFp8`` (run over the quantised
-    rows) or a ``SharedExpert`` (run over ``x``)."""
+    rows), or a ``SharedExpert`` or ``SharedExpertInt8`` (run over ``x``)."""
     _same_experts(gate_up, down)
     rows, top_k = topk_ids.shape
     hidden, mi = gate_up.k, gate_up.n // 2
@@ -1333,6 +1697,6 @@ def moe_layer_fp8(x, topk_ids, topk_weights, gate_up: Fp8ExpertTable, down: Fp8E
                           stream=stream)
     if isinstance(shared, SharedExpertFp8):
         shared = shared(xq, xs, limit, stream)
-    elif isinstance(shared, SharedExpert):
+    elif isinstance(shared, (SharedExpert, SharedExpertInt8)):
         shared = shared.for_combine(x, limit, stream)
     moe_combine(ws.expert_out[:s], ws.token_to_perm, topk_weights, out, shared, stream)

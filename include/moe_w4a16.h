@@ -28,6 +28,14 @@
  *                           scale per block of 128 (W8A8)
  *   moe_dense_gemm_fp8, moe_dense_gate_up_swiglu_fp8
  *                           the shared expert in the same format
+ *   moe_rmsnorm_bf16, moe_rmsnorm_fp8, moe_rmsnorm_int8
+ *                           the residual's addition and the root-mean-square norm before the
+ *                           layer, its rows in BF16 and in the form the products take
+ *   moe_quant_int8          rows to INT8, one scale per row
+ *   moe_dense_gemm_int8, moe_dense_gate_up_swiglu_int8
+ *                           the shared expert in INT8 (one scale per token and channel)
+ *   moe_shared_expert_int8  the whole shared expert in INT8
+ *   moe_w4a16_layer_few     a whole routed layer for a few tokens in two kernels
  *
  * Sources (the pages this library follows, by title and section):
  *   [FPG]  "Module forward_prefill_gemm" (glm5next_mlp/forward_prefill_gemm), sections
@@ -713,6 +721,181 @@ int moe_w8a8_grouped_gemm_swiglu(const uint8_t *a, int64_t lda, const float *a_s
                                  int64_t ld_act_scale, int32_t max_rows, int32_t mi, int32_t k,
                                  float limit, void *workspace, int64_t workspace_bytes,
                                  void *stream);
+
+/*
+ * moe_rmsnorm_bf16, moe_rmsnorm_fp8, moe_rmsnorm_int8 - the residual's addition and the
+ * root-mean-square norm that make a layer's rows, in one launch:
+ *
+ *   h[r, c] = bf16( x[r, c] + residual[r, c] )          (x itself without a residual)
+ *   y[r, c] = h[r, c] * weight[c] / sqrt( mean_c(h[r, c]^2) + eps )             (FP32)
+ *   moe_rmsnorm_bf16   stores bf16(y)
+ *   moe_rmsnorm_fp8    stores E4M3 codes with one FP32 scale per 128 columns, as moe_quant_fp8
+ *                      does: scale = max(amax / 448, 2^-126), code = e4m3(y / scale)
+ *   moe_rmsnorm_int8   stores INT8 codes with one FP32 scale per row, as moe_quant_int8 does:
+ *                      scale = max(amax / 127, 2^-126), code = rint(y / scale)
+ *
+ * The norm is of the stored (rounded) sum h; y is not rounded before it is quantised. With eps
+ * 0, a row of zeros gives NaN. A NaN in a row makes the row's outputs NaN (INT8: its scale).
+ * Magnitudes stay within FP32 as long as |h weight| and the sum of h^2 do.
+ *
+ *   x         bf16 [rows, ld_x]
+ *   residual  bf16 [rows, ld_res] or NULL
+ *   weight    bf16 [cols]
+ *   h         bf16 [rows, ld_h] or NULL (not stored)   out: the new residual stream
+ *   y         bf16 [rows, ld_y], or NULL in the quantised forms (not stored)   out
+ *   q         E4M3 or INT8 codes [rows, ld_q]   out
+ *   scale     float [rows, ld_scale] (E4M3), float [rows] (INT8)   out
+ * h may be x or residual themselves (same pointer and leading dimension), y may be x; other
+ * overlaps of outputs with inputs are not allowed.
+ * Requirements (else MOE_EINVAL): 0 <= rows < 2^22; cols >= 0, a multiple of 8; eps finite and
+ * >= 0; leading dimensions >= cols and multiples of 8; ld_scale >= ceil(cols / 128); x,
+ * residual, weight, h and y 16-byte aligned, q 8-byte, scale 4-byte; required pointers
+ * non-NULL when rows * cols > 0.
+ */
+int moe_rmsnorm_bf16(const uint16_t *x, int64_t ld_x, const uint16_t *residual, int64_t ld_res,
+                     const uint16_t *weight, float eps, uint16_t *h, int64_t ld_h, uint16_t *y,
+                     int64_t ld_y, int32_t rows, int32_t cols, void *stream);
+int moe_rmsnorm_fp8(const uint16_t *x, int64_t ld_x, const uint16_t *residual, int64_t ld_res,
+                    const uint16_t *weight, float eps, uint16_t *h, int64_t ld_h, uint16_t *y,
+                    int64_t ld_y, uint8_t *q, int64_t ld_q, float *scale, int64_t ld_scale,
+                    int32_t rows, int32_t cols, void *stream);
+int moe_rmsnorm_int8(const uint16_t *x, int64_t ld_x, const uint16_t *residual, int64_t ld_res,
+                     const uint16_t *weight, float eps, uint16_t *h, int64_t ld_h, uint16_t *y,
+                     int64_t ld_y, int8_t *q, int64_t ld_q, float *scale, int32_t rows,
+                     int32_t cols, void *stream);
+
+/*
+ * moe_quant_int8 - BF16 rows to INT8 codes with one FP32 scale per row:
+ *   scale[r] = max(max_c |x[r, c]| / 127, 2^-126),   q[r, c] = rint(x[r, c] / scale[r])
+ * in FP32, divisions and rounding as IEEE does them (ties to even), codes in [-127, 127]. A row
+ * with a NaN or an infinity gets a NaN or infinite scale and codes 0.
+ *
+ *   x bf16 [rows, ld_x], q int8 [rows, ld_q], scale float [rows]
+ * Requirements (else MOE_EINVAL): those of moe_rmsnorm_int8 on x, q, scale, rows and cols.
+ */
+int moe_quant_int8(const uint16_t *x, int64_t ld_x, int8_t *q, int64_t ld_q, float *scale,
+                   int32_t rows, int32_t cols, void *stream);
+
+/* Largest k of the INT8 products: their sums stay within 32 bits for codes down to -128. */
+#define MOE_INT8_MAX_K 131056
+
+/*
+ * moe_dense_gemm_int8 - the product of INT8 rows and an INT8 weight with FP32 scales per token
+ * (row) and per output channel:
+ *
+ *   c[m, n] = bf16( (float( sum_k a[m, k] * b[n, k] ) * a_scale[m]) * b_scale[n] )
+ *
+ * The sum is exact (32-bit integers); its conversion and the two products round to FP32.
+ *
+ *   a        int8 [m, lda]  rows, as moe_quant_int8 or moe_rmsnorm_int8 leave them
+ *   a_scale  float [m]
+ *   b        int8 [n, ldb]  the weight, one row per output channel
+ *   b_scale  float [n]
+ *   c        bf16 [m, ldc]
+ * Requirements (else MOE_EINVAL): m >= 0; n > 0 and k > 0 multiples of 16, k <= MOE_INT8_MAX_K;
+ * lda >= k and ldb >= k, multiples of 16 below 2^22; ldc >= n and a multiple of 4; a and b
+ * 16-byte, c 8-byte and the scales 4-byte aligned, all non-NULL when m > 0.
+ */
+int moe_dense_gemm_int8(const int8_t *a, int64_t lda, const float *a_scale, const int8_t *b,
+                        int64_t ldb, const float *b_scale, uint16_t *c, int64_t ldc, int32_t m,
+                        int32_t n, int32_t k, void *stream);
+
+/*
+ * moe_dense_gate_up_swiglu_int8 - the shared expert's gate and up products and the clamped
+ * SwiGLU in one launch. G and U are the FP32 values moe_dense_gemm_int8 would round:
+ *
+ *   act[m, j] = bf16( silu(min(G, limit)) * clamp(U, -limit, limit) ),   j in [0, inter)
+ *
+ *   gate_w, up_w          int8 [inter, ldw]
+ *   gate_scale, up_scale  float [inter]
+ *   act                   bf16 [m, ld_act]
+ * Requirements (else MOE_EINVAL): limit > 0; those of moe_dense_gemm_int8 with n = inter.
+ */
+int moe_dense_gate_up_swiglu_int8(const int8_t *a, int64_t lda, const float *a_scale,
+                                  const int8_t *gate_w, const float *gate_scale,
+                                  const int8_t *up_w, const float *up_scale, int64_t ldw,
+                                  uint16_t *act, int64_t ld_act, int32_t m, int32_t inter,
+                                  int32_t k, float limit, void *stream);
+
+/*
+ * moe_shared_expert_int8 - the whole shared expert in INT8 on quantised rows: gate and up
+ * products and SwiGLU as moe_dense_gate_up_swiglu_int8, its FP32 values quantised per row as
+ * moe_quant_int8 quantises (not rounded to BF16 first), and the down product as
+ * moe_dense_gemm_int8. Three kernels.
+ *
+ *   a, a_scale     INT8 rows [m, lda] and their scales
+ *   gate_*, up_*   int8 [inter, ldw], float [inter];  down_*  int8 [hidden, ld_down], float [hidden]
+ *   out            bf16 [m, ld_out]
+ *   workspace      moe_shared_expert_int8_workspace_bytes(m, inter) bytes, 256-byte aligned, the
+ *                  caller's; calls that share one must be ordered on one stream
+ * Requirements (else MOE_EINVAL / MOE_ECAPACITY): m < 2^22; those of the three calls; workspace
+ * non-NULL, aligned and large enough when m > 0.
+ */
+int moe_shared_expert_int8(const int8_t *a, int64_t lda, const float *a_scale,
+                           const int8_t *gate_w, const float *gate_scale, const int8_t *up_w,
+                           const float *up_scale, int64_t ldw, const int8_t *down_w,
+                           int64_t ld_down, const float *down_scale, uint16_t *out,
+                           int64_t ld_out, int32_t m, int32_t inter, int32_t hidden, float limit,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Bytes of moe_shared_expert_int8's workspace; 0 without rows or columns. */
+int64_t moe_shared_expert_int8_workspace_bytes(int32_t m, int32_t inter);
+
+/* Limits of moe_w4a16_layer_few: rows, rows * top_k, hidden, mi. */
+#define MOE_FEW_MAX_ROWS 16
+#define MOE_FEW_MAX_IDS 256
+#define MOE_FEW_MAX_HIDDEN 8192
+#define MOE_FEW_MAX_MI 65536
+
+/*
+ * moe_w4a16_layer_few - a whole routed NVFP4 layer for a few tokens (decode, verify) in two
+ * kernels: the router (optional), gate_up with the clamped SwiGLU, down, the weighted sum over
+ * a row's slots and the shared term:
+ *
+ *   G, U        = (sum_k x[r, k] q[n, k] d[n, k / 16]) * gate_up_scale2[e]
+ *   act[slot]   = bf16( silu(min(G, limit)) * clamp(U, -limit, limit) )
+ *   out[r, h]   = bf16( sum_slot topk_weights[slot] * down_scale2[e] *
+ *                       (sum_k act[slot, k] q[h, k] d[h, k / 16])  + shared[r, h] )
+ *
+ * with q the E2M1 value and d the E4M3 block scale of a weight (tables as in
+ * moe_w4a16_grouped_gemm and its SwiGLU form). A weight is the exact product q d; unlike the
+ * other calls, scale2 multiplies the FP32 sums and is not rounded into a BF16 weight, and the
+ * gate_up values and the experts' outputs are not rounded to BF16 on the way. Sums are FP32, in
+ * a fixed order for given inputs that depends on the experts of all rows.
+ *
+ * With logits, the routing is moe_router_topk's (its arguments; num_experts <=
+ * MOE_ROUTER_MAX_EXPERTS, top_k <= MOE_ROUTER_MAX_TOPK; above 512 experts the router is a launch
+ * of its own) and is written to topk_ids and topk_weights where they are given; without, they
+ * are read. A slot whose id is outside [0, num_experts), whose expert has a null entry in one of
+ * the tables, or that repeats an id of its row adds nothing.
+ *
+ *   x             bf16 [rows, ld_x]
+ *   logits        float [rows, ld_logits] or NULL;  bias float [num_experts] or NULL
+ *   topk_ids      int32 [rows * top_k];  topk_weights float [rows * top_k]
+ *   gate_up_*     tables of [2 mi, hidden] weights (gate rows, then up rows)
+ *   down_*        tables of [hidden, mi] weights
+ *   shared        bf16 [rows, ld_shared] or NULL
+ *   out           bf16 [rows, ld_out]; may be shared itself
+ *   workspace     moe_few_workspace_bytes(rows, top_k, mi) bytes, the caller's; calls that share
+ *                 one must be ordered on one stream
+ * Requirements (else MOE_EINVAL / MOE_ECAPACITY): 0 <= rows <= MOE_FEW_MAX_ROWS; top_k >= 1, rows
+ * * top_k <= MOE_FEW_MAX_IDS; hidden and mi positive multiples of 64, at most MOE_FEW_MAX_HIDDEN
+ * and MOE_FEW_MAX_MI; limit > 0; ld_x >= hidden, a multiple of 8, below 2^24; ld_out and
+ * ld_shared >= hidden, multiples of 4; x and workspace 16-byte, out and shared 8-byte aligned;
+ * required pointers non-NULL when rows > 0; workspace_bytes large enough. Table addresses as in
+ * moe_w4a16_grouped_gemm.
+ */
+int moe_w4a16_layer_few(
+    const uint16_t *x, int64_t ld_x, const float *logits, int64_t ld_logits, const float *bias,
+    float routed_scale, int32_t renormalize, int32_t *topk_ids, float *topk_weights,
+    const uint64_t *gate_up_packed, const uint64_t *gate_up_scales, const float *gate_up_scale2,
+    const uint64_t *down_packed, const uint64_t *down_scales, const float *down_scale2,
+    int32_t num_experts, const uint16_t *shared, int64_t ld_shared, uint16_t *out, int64_t ld_out,
+    int32_t rows, int32_t top_k, int32_t hidden, int32_t mi, float limit, void *workspace,
+    int64_t workspace_bytes, void *stream);
+
+/* Bytes of moe_w4a16_layer_few's workspace; 0 for sizes it does not take. */
+int64_t moe_few_workspace_bytes(int32_t rows, int32_t top_k, int32_t mi);
 
 #ifdef __cplusplus
 }
