@@ -7,16 +7,27 @@
 //
 // Because the sums are exact, every tile, split and order of K gives the same bits.
 //
-// Two kernels:
-//   - few rows (m <= 64): the weights stream from memory straight into the registers of the
-//     matrix instruction, K split over the waves of a block;
-//   - tiles: stages of 128 k (KS of them side by side) loaded straight into LDS, ST - 1 ahead.
-// The product is v_mfma_i32_16x16x64_i8 with weights as operand A and rows as B: a lane holds 4
+// Two kernels (which one and which tile: int8_plan.h):
+//   - tile_kernel, up to 128 x 128: stages of 128 k (KS of them side by side, multiplied by as
+//     many groups of waves) loaded straight into LDS, ST - 1 ahead;
+//   - wide_kernel, 256 rows: persistent blocks in which half of the waves reads while the other
+//     half multiplies.
+// Weights are the matrix instruction's operand A and rows its operand B: a lane holds 4
 // consecutive outputs of one row.
+//
+// What bounds it (256 CUs):
+//   - One row to some dozens: the weights from memory, the start of a block and of a launch: 6144 x
+//     2048 in 3.4 us of kernel (1 to 16 rows, weights in the last-level cache; 5.0 from memory).
+//   - Hundreds: what a CU takes in from its L2 (36 bytes a clock): 256 rows in 8.2 us.
+//   - Thousands: power. At 4096 x 6144 x 2048 the chip runs at 1.45 to 1.7 GHz of its 2.4; a step of
+//     the 192 x 256 tile takes 1980 clocks of which 1536 are products. 54 to 64 us by the
+//     codes' size (small codes toggle fewer bits), 1600 to 1900 TOPS; 8192^3 at 2200.
+#include <algorithm>
+
 #include "buffer_io.h"
 #include "common.h"
-#include "fp8.h"  // fp8_swiglu
 #include "int8.h"
+#include "int8_plan.h"
 #include "lds_limit.h"
 #include "nvfp4_decode.h"  // moe::pack_bf16x2
 
@@ -27,10 +38,12 @@ using moe::make_rsrc;
 using moe::u32x4_t;
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kRowBytes = 128;  // one LDS row: 128 k
 constexpr int kMaxK = MOE_INT8_MAX_K;
 constexpr int kGroupM = 4;  // row tiles that run next to each other
+constexpr int kCus = 256;
 
 struct GemmArgs {
   const int8_t *a;       // [m, lda]
@@ -65,84 +78,16 @@ __device__ __forceinline__ float scaled(int sum, float sa, float sw) {
   return (static_cast<float>(sum) * sa) * sw;
 }
 
-// ------------------------------------------------------------------------------ few rows
-
-// A block owns 16 weight rows (8 gate and the same 8 up rows in the SwiGLU form) and all m <=
-// 16 TT rows; wave w takes the chunks of 128 k w, w + kWaves, ... Both operands come straight
-// into registers: lane (r16, g4) loads 16 bytes of row r16 at k 16 g4 and 64 + 16 g4 of a
-// chunk, whole 128-byte lines per row.
-template <int TT, int kWaves, bool kSwiglu>
-__global__ __launch_bounds__(64 * kWaves) void few_kernel(GemmArgs p) {
-  constexpr int kAhead = TT >= 4 ? 2 : 4;  // chunks in flight per wave
-  constexpr int kOut = kSwiglu ? 8 : 16;   // output columns
-  __shared__ __attribute__((aligned(16))) i32x4_t red[kWaves][TT][64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r16 = lane & 15, g4 = lane >> 4;
-  const int n0 = blockIdx.x * kOut;
-  const uint32_t ldw = static_cast<uint32_t>(p.ldw), lda = static_cast<uint32_t>(p.lda);
-  // n is a multiple of 16: the tile's columns all exist.
-  const int wr = kSwiglu ? r16 & 7 : r16;
-  const int8_t *w_base = p.w0 + static_cast<int64_t>(n0) * p.ldw;
-  const int8_t *u_base = (kSwiglu ? p.w1 : p.w0) + static_cast<int64_t>(n0) * p.ldw;
-  const int8_t *w_row = (kSwiglu && r16 >= 8 ? u_base : w_base) + static_cast<int64_t>(wr) * ldw;
-  const __amdgpu_buffer_rsrc_t x_rsrc = make_rsrc(p.a, static_cast<uint32_t>(p.m) * lda);
-
-  i32x4_t acc[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) acc[t] = i32x4_t{0, 0, 0, 0};
-  const int chunks = (p.k + 127) / 128;
-  for (int c0 = wave; c0 < chunks; c0 += kWaves * kAhead) {
-    u32x4_t w[kAhead][2], x[kAhead][2][TT];
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int k = (c0 + u * kWaves) * 128 + 64 * h + 16 * g4;  // past K: zeros
-        w[u][h] = u32x4_t{0u, 0u, 0u, 0u};
-        if (k < p.k) w[u][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(w_row + k));
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          const uint32_t off = static_cast<uint32_t>(16 * t + r16) * lda + static_cast<uint32_t>(k);
-          x[u][h][t] = moe::load16(x_rsrc, k < p.k ? off : kNoLoad, 0);
-        }
-      }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < TT; ++t) acc[t] = mma(w[u][h], x[u][h][t], acc[t]);
-  }
-#pragma unroll
-  for (int t = 0; t < TT; ++t) red[wave][t][lane] = acc[t];
-  __syncthreads();
-  for (int t = wave; t < TT; t += kWaves) {  // wave-uniform
-    i32x4_t sum = red[0][t][lane];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += red[w][t][lane];
-    const int row = 16 * t + r16;
-    const bool live = row < p.m;
-    const float sa = live ? p.a_scale[row] : 0.0f;
-    float y[4];
-    if (kSwiglu) {
-      const int col = n0 + 4 * (g4 & 1);
-      float up[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float *s = g4 < 2 ? p.s0 : p.s1;
-        y[x] = scaled(sum[x], sa, s[col + x]);
-        up[x] = __shfl_xor(y[x], 32, 64);
-        y[x] = moe::fp8_swiglu(y[x], up[x], p.limit);
-      }
-      if (live && g4 < 2) store4<true>(p, row, col, y);
-    } else {
-      const int col = n0 + 4 * g4;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) y[x] = scaled(sum[x], sa, p.s0[col + x]);
-      if (live) store4<false>(p, row, col, y);
-    }
-  }
+// silu(min(g, L)) * clamp(u, -L, L), NaN kept by the IEEE minimum and maximum, in 15 operations (the
+// large tiles' epilogues are bound by them: 28 took 91 us where these take 87 at 4096 rows, width
+// 2048, K 6144). The rounding of the exponential's argument moves the result by |g| 2^-24 of
+// itself; below g = -88.7 the exponential of -g overflows and the result is 0 (it is below
+// 3e-37 L there).
+__device__ __forceinline__ float swiglu(float g, float u, float limit) {
+  const float gc = __builtin_elementwise_minimum(g, limit);
+  const float uc = __builtin_elementwise_maximum(__builtin_elementwise_minimum(u, limit), -limit);
+  const float e = __builtin_amdgcn_exp2f(gc * -1.44269504f);  // log2(e)
+  return gc * __builtin_amdgcn_rcpf(1.0f + e) * uc;
 }
 
 // --------------------------------------------------------------------------------- tiles
@@ -331,10 +276,259 @@ __global__ __launch_bounds__(C::kThreads, C::kMinWaves) void tile_kernel(GemmArg
       const i32x4_t up = sums(kBnOut + q);
 #pragma unroll
       for (int x = 0; x < 4; ++x)
-        y[x] = moe::fp8_swiglu(y[x], scaled(up[x], sa, p.s1[n0 + q + x]), p.limit);
+        y[x] = swiglu(y[x], scaled(up[x], sa, p.s1[n0 + q + x]), p.limit);
     }
     store4<kSwiglu>(p, m0 + r, n0 + q, y);
   }
+}
+
+// ---------------------------------------------------------------------------- large tiles
+
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+// NT 32-row weight tiles and TT 32-row row tiles per wave, WN x WT = 8 waves, two stages of 128 k.
+template <int NT_, int TT_, int WN_, int WT_>
+struct WideCfg {
+  static constexpr int NT = NT_, TT = TT_, WN = WN_, WT = WT_;
+  static constexpr int BN = 32 * NT * WN, BT = 32 * TT * WT;
+  static constexpr int kWaves = WN * WT, kThreads = 64 * kWaves;
+  static constexpr int kWBytes = BN * kRowBytes, kStage = (BN + BT) * kRowBytes;
+  static constexpr int kOutBytes = 32 * 64 * NT;  // a wave's 32 rows of 32 NT BF16 outputs
+  static constexpr int kLds = 2 * kStage + kWaves * kOutBytes;
+  static constexpr int kWLoads = BN / 8 / kWaves, kXLoads = BT / 8 / kWaves;
+  static constexpr int kLoads = kWLoads + kXLoads;
+  static_assert(kWaves == 8, "two waves per SIMD, one of each group");
+  static_assert(BN / 8 % kWaves == 0 && BT / 8 % kWaves == 0, "whole instructions");
+  static_assert(kLds <= 160 * 1024, "LDS");
+};
+
+__device__ __forceinline__ i32x16_t mma_wide(u32x4_t w, u32x4_t x, i32x16_t d) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, w),
+                                               __builtin_bit_cast(i32x4_t, x), d, 0, 0, 0);
+}
+
+// Persistent blocks, one per CU. Two phases per step of 128 k and wave: read the step's operands
+// from LDS, then multiply. Waves 0-3 and 4-7 (one of each on every SIMD) run them in opposite
+// order, the second group one barrier behind, so that a SIMD's matrix core is fed by one wave
+// while the other reads. In slots between barriers, step s is read in slot 2 s by the first group
+// and in 2 s + 1 by the second, and multiplied in the slot after. The buffer of stage s - 1 is
+// free from slot 2 s on: there both groups issue their loads of stage s + 1 (the first beside its
+// reads, the second between its products), and both have waited for them when slot 2 s + 1
+// ends. Steps are counted through all of a block's tiles, so a tile's first stages are loaded
+// during the last steps of the one before; a finished tile's outputs take one more slot of each
+// group, and their stores are waited for behind the next tile's first loads.
+template <class C, bool kSwiglu>
+__global__ __launch_bounds__(C::kThreads, 2) void wide_kernel(GemmArgs p) {
+  constexpr int NT = C::NT, TT = C::TT, WN = C::WN, WT = C::WT, BN = C::BN, BT = C::BT;
+  constexpr int kBnOut = kSwiglu ? BN / 2 : BN;
+  static_assert(!kSwiglu || NT == 2, "a gate tile and its up tile per wave");
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave % WN, wt = wave / WN, group = wave / 4;
+  const int rl = lane & 31, gl = lane >> 5;
+  const uint32_t m_tiles = (p.m + BT - 1) / BT, n_tiles = (p.n + kBnOut - 1) / kBnOut;
+  const uint32_t total = m_tiles * n_tiles;
+  const int steps = (p.k + kRowBytes - 1) / kRowBytes;
+  const int8_t *w_src = kSwiglu && 8 * wave * C::kWLoads >= kBnOut ? p.w1 : p.w0;
+
+  // Instruction i fills the 8 LDS rows from 8 i on; row r holds its logical piece c at c ^ (r / 2 %
+  // 8): the 32-row operand reads below then hit every bank once. So lane l loads piece (l % 8) ^
+  // (l / 16) of row l / 8, or that ^ 4 where i is odd.
+  const uint32_t w_lane = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(p.ldw);
+  const uint32_t x_lane = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(p.lda);
+  const uint32_t piece16 = 16u * ((lane & 7) ^ (lane >> 4));
+  // What is loaded next: a step of a tile, and the stage buffer it goes to. Past the last tile
+  // the buffers have no bytes.
+  struct Next {
+    uint32_t item;
+    int step, buf;
+    __amdgpu_buffer_rsrc_t w, x;
+  };
+  Next next;
+  const auto aim = [&]() __attribute__((always_inline)) {
+    const bool in = next.item < total;
+    const Tile t = tile_of(in ? next.item : 0, m_tiles, n_tiles, BT, kBnOut);
+    const int cnt = min(BT, p.m - t.m0), n_valid = min(kBnOut, p.n - t.n0);
+    next.w = make_rsrc(uniform(w_src + static_cast<int64_t>(t.n0) * p.ldw),
+                       in ? static_cast<uint32_t>(n_valid * p.ldw) : 0u);
+    next.x = make_rsrc(uniform(p.a + static_cast<int64_t>(t.m0) * p.lda),
+                       in ? static_cast<uint32_t>(cnt * p.lda) : 0u);
+  };
+  const auto load = [&](int n) __attribute__((always_inline)) {
+    uint8_t *st = lds + next.buf;
+    const int k0 = next.step * kRowBytes;
+    const bool is_w = n < C::kWLoads;
+    const int inst = is_w ? wave * C::kWLoads + n : wave * C::kXLoads + n - C::kWLoads;
+    const uint32_t at = piece16 ^ (64u * (inst & 1));
+    const uint32_t dead = static_cast<int>(at) < p.k - k0 ? 0u : kNoLoad;  // past K: zeros
+    if (is_w) {
+      const int row = kSwiglu ? 8 * inst % kBnOut : 8 * inst;
+      load_lds16(next.w, st + 1024 * inst,
+                 (w_lane + static_cast<uint32_t>(row) * static_cast<uint32_t>(p.ldw) + at) | dead, k0);
+    } else {
+      load_lds16(next.x, st + C::kWBytes + 1024 * inst,
+                 (x_lane + static_cast<uint32_t>(8 * inst) * static_cast<uint32_t>(p.lda) + at) | dead,
+                 k0);
+    }
+  };
+  const auto advance = [&]() __attribute__((always_inline)) {
+    next.buf ^= C::kStage;
+    if (++next.step == steps) {  // uniform
+      next.step = 0;
+      next.item += gridDim.x;
+      aim();
+    }
+  };
+  next.item = blockIdx.x;
+  next.step = next.buf = 0;
+  aim();
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+#pragma unroll
+    for (int n = 0; n < C::kLoads; ++n) load(n);
+    advance();
+  }
+
+  // acc[i][t][4 g + x]: tile column w_row(i) + 8 g + 4 gl + x of tile row 32 (t WT + wt) + rl.
+  const auto w_row = [&](int i) {
+    return kSwiglu ? i * kBnOut + wn * 32 : (wn * NT + i) * 32;
+  };
+  int frag[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) frag[j] = rl * kRowBytes + 16 * ((2 * j + gl) ^ ((rl >> 1) & 7));
+  constexpr int kStageWait = (C::kLoads & 15) | ((C::kLoads >> 4) << 14) | (7 << 4) | (15 << 8);
+  constexpr int kLoadsDone = (7 << 4) | (15 << 8);        // vmcnt(0)
+  constexpr int kReadsDone = 15 | (3 << 14) | (7 << 4);    // lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt(kStageWait);  // stage 0
+  __builtin_amdgcn_s_barrier();
+  if (group == 1) __builtin_amdgcn_s_barrier();
+  int buf = 0;
+  bool started = false;  // the first two stages are loaded above
+  for (uint32_t item = blockIdx.x; item < total; item += gridDim.x) {
+    i32x16_t acc[NT][TT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[i][t] = i32x16_t{};
+    for (int s = 0; s < steps; ++s) {
+      // Read (slot 2 s + group).
+      if (group == 0 && started) {
+#pragma unroll
+        for (int n = 0; n < C::kLoads; ++n) load(n);
+        advance();
+      }
+      started = true;
+      const uint8_t *ws = lds + buf;
+      const uint8_t *xs = ws + C::kWBytes + wt * 32 * kRowBytes;
+      buf ^= C::kStage;
+      u32x4_t w[NT][4], x[TT][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          w[i][j] = *reinterpret_cast<const u32x4_t *>(ws + w_row(i) * kRowBytes + frag[j]);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          x[t][j] = *reinterpret_cast<const u32x4_t *>(xs + t * WT * 32 * kRowBytes + frag[j]);
+      }
+      __builtin_amdgcn_s_waitcnt(kReadsDone);
+      if (group == 1) __builtin_amdgcn_s_waitcnt(kLoadsDone);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      // Multiply (slot 2 s + 1 + group).
+      __builtin_amdgcn_s_setprio(1);  // before the reading wave of the SIMD: 1 to 2 %
+      constexpr int kProducts = 4 * NT * TT;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            acc[i][t] = mma_wide(w[i][j], x[t][j], acc[i][t]);
+            if (group == 1) {  // a load behind every few products
+              const int q = (j * TT + t) * NT + i;
+              if ((q + 1) * C::kLoads / kProducts > q * C::kLoads / kProducts)
+                load(q * C::kLoads / kProducts);
+            }
+          }
+      __builtin_amdgcn_s_setprio(0);
+      if (group == 1) advance();
+      if (group == 0) __builtin_amdgcn_s_waitcnt(kLoadsDone);
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    }
+
+    // The tile's outputs, 32 rows at a time through the wave's own piece of LDS, so that rows
+    // leave in whole 64- to 192-byte pieces. Its 16-byte pieces are permuted within a row so that
+    // neither side meets a bank more often than it must.
+    constexpr int kCols = kSwiglu ? 32 : 32 * NT;  // the wave's output columns
+    constexpr int kOutRow = 2 * kCols, kLanes = kCols / 8;
+    const auto place = [](int r, int piece) {
+      return r * kOutRow + 16 * (piece ^ (kLanes == 8 ? r & 7 : (r >> 1) & 3));
+    };
+    const Tile tile = tile_of(item, m_tiles, n_tiles, BT, kBnOut);
+    const int cnt = min(BT, p.m - tile.m0);
+    uint8_t *mine = lds + 2 * C::kStage + wave * C::kOutBytes;
+    const int col0 = tile.n0 + wn * kCols;
+    // Every scale at once: a load per value would be waited for one after the other.
+    f32x4_t sw[NT][4];
+    float sa[TT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float *src = kSwiglu && i == 1 ? p.s1 : p.s0;
+        const int c = col0 + (kSwiglu ? 0 : 32 * i) + 8 * g + 4 * gl;
+        __builtin_memcpy(&sw[i][g], src + min(c, p.n - 4), 16);  // 4-byte aligned
+      }
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      sa[t] = p.a_scale[tile.m0 + min(32 * (t * WT + wt) + rl, cnt - 1)];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const int r0 = 32 * (t * WT + wt);
+#pragma unroll
+      for (int i = 0; i < (kSwiglu ? 1 : NT); ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int c = 32 * i + 8 * g + 4 * gl;  // of the wave's columns
+          float y[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            y[q] = scaled(acc[i][t][4 * g + q], sa[t], sw[i][g][q]);
+            if constexpr (kSwiglu)
+              y[q] = swiglu(y[q], scaled(acc[1][t][4 * g + q], sa[t], sw[1][g][q]),
+                                     p.limit);
+          }
+          if (kSwiglu && p.c32 != nullptr) {
+            if (col0 + c < p.n && r0 + rl < cnt)
+              store4<true>(p, tile.m0 + r0 + rl, col0 + c, y);
+          } else {
+            *reinterpret_cast<uint2 *>(mine + place(rl, 4 * i + g) + 8 * gl) =
+                make_uint2(moe::pack_bf16x2(y[0], y[1]), moe::pack_bf16x2(y[2], y[3]));
+          }
+        }
+      if (kSwiglu && p.c32 != nullptr) continue;
+#pragma unroll
+      for (int u = 0; u < 32 * kLanes; u += 64) {
+        const int r = (u + lane) / kLanes, piece = (u + lane) % kLanes, c = 8 * piece;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(mine + place(r, piece));
+        if (r0 + r < cnt && col0 + c < p.n) {  // n is a multiple of 16
+          uint16_t *dst = p.c + static_cast<int64_t>(tile.m0 + r0 + r) * p.ldc + col0 + c;
+          // ldc may be any multiple of 4 (one 16-byte store where it can be was no faster)
+          reinterpret_cast<uint2 *>(dst)[0] = make_uint2(v[0], v[1]);
+          reinterpret_cast<uint2 *>(dst)[1] = make_uint2(v[2], v[3]);
+        }
+      }
+    }
+    __builtin_amdgcn_s_barrier();  // the slot of the outputs
+    asm volatile("" ::: "memory");
+  }
+  if (group == 0) __builtin_amdgcn_s_barrier();
+  // The past-the-end stages' loads write LDS (zeros) too: they finish first.
+  __builtin_amdgcn_s_waitcnt(0);
 }
 
 template <class C, bool kSwiglu>
@@ -351,20 +545,42 @@ int launch_tile(const char *name, const GemmArgs &p, void *stream) {
                      stream, p);
 }
 
-template <int TT, int kWaves, bool kSwiglu>
-int launch_few(const char *name, const GemmArgs &p, void *stream) {
-  const unsigned blocks = static_cast<unsigned>(p.n / (kSwiglu ? 8 : 16));
-  return moe::launch(name, few_kernel<TT, kWaves, kSwiglu>, dim3(blocks), dim3(64 * kWaves), 0,
-                     stream, p);
+template <class C, bool kSwiglu>
+int launch_wide(const char *name, const GemmArgs &p, void *stream) {
+  constexpr int kBnOut = kSwiglu ? C::BN / 2 : C::BN;
+  const int64_t tiles = static_cast<int64_t>((p.m + C::BT - 1) / C::BT) *
+                        ((p.n + kBnOut - 1) / kBnOut);
+  MOE_REQUIRE(tiles < (1ll << 31), "%s: matrix too large", name);
+  constexpr auto kern = wide_kernel<C, kSwiglu>;
+  MOE_REQUIRE_CODE(moe::allow_lds<kern>(C::kLds), MOE_ELAUNCH, "%s: %d bytes of LDS were refused",
+                   name, C::kLds);
+  return moe::launch(name, kern, dim3(static_cast<unsigned>(std::min<int64_t>(tiles, kCus))),
+                     dim3(C::kThreads), C::kLds, stream, p);
 }
 
 template <bool kSwiglu>
 int launch_gemm(const char *name, const GemmArgs &p, void *stream) {
-  if (p.m <= 16) return launch_few<1, 8, kSwiglu>(name, p, stream);
-  if (p.m <= 32) return launch_few<2, 8, kSwiglu>(name, p, stream);
-  if (p.m <= 64) return launch_few<4, 8, kSwiglu>(name, p, stream);
-  if (p.m <= 512) return launch_tile<Cfg<2, 2, 2, 2, 2, 3>, kSwiglu>(name, p, stream);
-  return launch_tile<Cfg<4, 4, 2, 2, 1, 2>, kSwiglu>(name, p, stream);
+  const moe::Int8Tile tile = moe::int8_tile(kSwiglu, p.m, p.n, p.k);
+  if constexpr (kSwiglu) {
+    if (tile == moe::kInt8Tile128x128Pair)
+      return launch_tile<Cfg<4, 4, 2, 2, 1, 2>, true>(name, p, stream);
+  } else {
+    if (tile == moe::kInt8Tile32x16)
+      return launch_tile<Cfg<1, 1, 2, 1, 4, 3>, false>(name, p, stream);
+    if (tile == moe::kInt8Tile128x256)
+      return launch_wide<WideCfg<2, 2, 2, 4>, false>(name, p, stream);
+    if (tile == moe::kInt8Tile192x256)
+      return launch_wide<WideCfg<3, 2, 2, 4>, false>(name, p, stream);
+  }
+  switch (tile) {
+    case moe::kInt8Tile32x32: return launch_tile<Cfg<2, 1, 1, 2, 4, 3>, kSwiglu>(name, p, stream);
+    case moe::kInt8Tile64x32: return launch_tile<Cfg<2, 1, 2, 2, 2, 4>, kSwiglu>(name, p, stream);
+    case moe::kInt8Tile64x64: return launch_tile<Cfg<2, 2, 2, 2, 2, 3>, kSwiglu>(name, p, stream);
+    case moe::kInt8Tile128x64: return launch_tile<Cfg<4, 2, 2, 2, 2, 3>, kSwiglu>(name, p, stream);
+    case moe::kInt8Tile128x128:
+      return launch_tile<Cfg<4, 4, 2, 2, 2, 2>, kSwiglu>(name, p, stream);
+    default: return launch_wide<WideCfg<2, 4, 4, 2>, kSwiglu>(name, p, stream);
+  }
 }
 
 int check_gemm(const char *name, const GemmArgs &p, bool swiglu) {

@@ -41,7 +41,7 @@ def quantise_int8(x):
 
 def int8_values(a, a_scale, w, w_scale):
     """FP32 values ``(float(sum) * a_scale) * w_scale`` of the exact integer sums."""
-    sums = np.asarray(a, np.int64) @ np.asarray(w, np.int64).T
+    sums = np.asarray(a, np.float64) @ np.asarray(w, np.float64).T  # integers below 2^53: exact
     v = sums.astype(np.float32) * np.asarray(a_scale, np.float32)[:, None]
     return (v * np.asarray(w_scale, np.float32)[None, :]).astype(np.float32)
 

@@ -35,7 +35,8 @@ def _wide(codes, pad=32):
 SIZES = [(1, 16, 16), (1, 6144, 2048), (2, 48, 144), (16, 272, 1040), (17, 96, 256), (32, 160, 2064),
          (33, 48, 384), (64, 1360, 1040), (65, 144, 128), (77, 1360, 1040), (128, 256, 400),
          (256, 528, 2048), (300, 272, 720), (512, 144, 16), (513, 400, 1168), (700, 1040, 528),
-         (1024, 768, 640), (1500, 2064, 272), (2049, 272, 144), (4096, 512, 256)]
+         (1024, 768, 640), (1500, 2064, 272), (2049, 272, 144), (4096, 512, 256), (40, 4112, 272),
+         (139, 5648, 144), (556, 6752, 144), (1121, 6768, 144), (1559, 7088, 144), (2689, 2256, 288)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
