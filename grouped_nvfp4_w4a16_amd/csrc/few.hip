@@ -263,7 +263,8 @@ __device__ __forceinline__ void route_row(const FewArgs &p, int row, const float
 
 // What a block knows of the routing, in LDS. Covered slots (id in range, expert present, no
 // earlier slot of the row with the same id) are grouped by expert, at most `cap` slots to an
-// entry; entries stand in the order of their first slots.
+// entry, in the order of the slots. Entries stand in the order of their first slots (up to 64 ids,
+// or more than kTable experts) or of their experts.
 struct Entry {
   uint64_t packed, scales;
   float scale2;
@@ -271,8 +272,10 @@ struct Entry {
 };
 
 __device__ __forceinline__ Entry entry_of(const Tables &t, int e) {
-  const bool both = t.packed[e] != 0 && t.other[e] != 0;
-  return {both ? t.packed[e] : 0, t.scales[e], t.scale2[e], 0};
+  const uint64_t packed = t.packed[e], other = t.other[e], scales = t.scales[e];
+  const float scale2 = t.scale2[e];  // all four on their way before one is looked at
+  const bool both = (packed != 0) & (other != 0);
+  return {both ? packed : 0, scales, scale2, 0};
 }
 
 struct Routing {
@@ -282,9 +285,11 @@ struct Routing {
   int32_t *num;      // [kWaves + 1], the last the number of entries
   int16_t *slot_of;  // [n_ids][16]: slot of row r in an entry, or -1
   int16_t *pos_of;   // [kThreads]: a covered slot's place in its entry
+  uint32_t *mask;    // [kTable]: the rows of an expert, over 64 ids and up to kTable experts
+  int16_t *base;     // [kTable]: its first entry
   int16_t *list;     // [n_ids][cap]: the entry's slots in order, -1 past them (cap < 16 only)
 
-  static constexpr int kFixed = kThreads * 6 + 64;
+  static constexpr int kFixed = kThreads * 6 + 64 + kTable * 6;
   static constexpr __host__ __device__ int bytes(int n_ids, int num_experts, int cap) {
     const int table = num_experts < kTable ? num_experts : kTable;
     return kFixed + static_cast<int>(sizeof(Entry)) * (n_ids + table) +
@@ -294,10 +299,12 @@ struct Routing {
   __device__ __forceinline__ Routing(uint8_t *lds, int n_ids, int num_experts) {
     id = reinterpret_cast<int32_t *>(lds);
     num = id + kThreads;
-    entry = reinterpret_cast<Entry *>(num + 16);
+    mask = reinterpret_cast<uint32_t *>(num + 16);
+    entry = reinterpret_cast<Entry *>(mask + kTable);
     table = entry + n_ids;
     pos_of = reinterpret_cast<int16_t *>(table + min(num_experts, kTable));
-    slot_of = pos_of + kThreads;
+    base = pos_of + kThreads;
+    slot_of = base + kTable;
     list = slot_of + n_ids * 16;
   }
 
@@ -312,6 +319,7 @@ struct Routing {
   __device__ __forceinline__ void begin(const FewArgs &p, const Entry &mine, int tid) {
     const int n_ids = p.rows * p.top_k;
     if (p.num_experts <= kTable && tid < p.num_experts) table[tid] = mine;
+    mask[tid] = 0;
     for (int q = tid; q < n_ids * 8; q += kThreads) reinterpret_cast<int32_t *>(slot_of)[q] = -1;
     if (kCap < kMaxRows)
       for (int q = tid; q < n_ids * kCap / 2; q += kThreads)
@@ -333,9 +341,11 @@ struct Routing {
   __device__ __forceinline__ void group(const FewArgs &p, const Tables &t, int tid) {
     const int n_ids = p.rows * p.top_k;
     const int lane = tid & 63, wave = tid >> 6;
-    if (n_ids <= 64 && wave != 0) return;  // one wave, without barriers
-    const int row = tid / p.top_k, j = tid - row * p.top_k;
-    int v = tid < n_ids ? id[tid] : -1;
+    // Up to 64 ids: the last wave, without barriers.
+    if (n_ids <= 64 && wave != kWaves - 1) return;
+    const int slot = n_ids <= 64 ? lane : tid;
+    const int row = slot / p.top_k, j = slot - row * p.top_k;
+    int v = slot < n_ids ? id[slot] : -1;
     Entry en = {0, 0, 0.0f, 0};
     if (v >= 0 && v < p.num_experts)
       en = p.num_experts <= kTable ? table[v] : entry_of(t, v);
@@ -368,18 +378,50 @@ struct Routing {
     }
     for (int jj = 0; jj < j && v >= 0; ++jj)
       if (id[row * p.top_k + jj] == v) v = -1;  // a repeat in the row
+    if (p.num_experts <= kTable) {
+      // Entries in the order of their experts: every expert's rows as a mask, its entries counted.
+      if (v >= 0) atomicOr(&mask[v], 1u << row);  // no order
+      __syncthreads();
+      const uint32_t rows = mask[tid];
+      const int mine = (__popc(rows) + kCap - 1) / kCap;
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(upto, d, 64);
+        if (lane >= d) upto += o;
+      }
+      if (lane == 63) num[wave] = upto;
+      __syncthreads();
+      int first = upto - mine, n = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        first += w < wave ? num[w] : 0;
+        n += num[w];
+      }
+      base[tid] = static_cast<int16_t>(first);
+      for (int q = 0; q < mine; ++q) entry[first + q] = table[tid];
+      if (tid == 0) num[kWaves] = n;
+      __syncthreads();
+      if (v >= 0) {
+        const int before = __popc(mask[v] & ((1u << row) - 1u));
+        put<kCap>(tid, row, before, base[v] + before / kCap);
+      }
+      return;
+    }
     __syncthreads();
     id[tid] = v;
     __syncthreads();
     int before = 0, opener = tid;
-    for (int q = 0; q < tid; q += 4) {
-      const int4 w = *reinterpret_cast<const int4 *>(id + q);
-      const int e[4] = {w.x, w.y, w.z, w.w};
+    if (wave * 64 < n_ids) {  // the slots before this one with its id
+      for (int q = 0; q < min(tid, n_ids); q += 4) {
+        const int4 w = *reinterpret_cast<const int4 *>(id + q);
+        const int e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const bool hit = v >= 0 && q + u < tid && e[u] == v;
-        opener = hit && before % kCap == 0 ? q + u : opener;
-        before += hit ? 1 : 0;
+        for (int u = 0; u < 4; ++u) {
+          const bool hit = v >= 0 && q + u < tid && e[u] == v;
+          opener = hit && before % kCap == 0 ? q + u : opener;
+          before += hit ? 1 : 0;
+        }
       }
     }
     const bool opens = v >= 0 && before % kCap == 0;
@@ -387,14 +429,14 @@ struct Routing {
     const uint64_t ballot = __ballot(opens);
     if (lane == 0) num[wave] = __popcll(ballot);
     __syncthreads();
-    int base = 0, n = 0;
+    int first = 0, n = 0;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      base += w < wave ? num[w] : 0;
+      first += w < wave ? num[w] : 0;
       n += num[w];
     }
     if (opens) {
-      const int e = base + __popcll(ballot & below);
+      const int e = first + __popcll(ballot & below);
       pos_of[tid] = static_cast<int16_t>(e);  // for now: the entry that the slot opened
       entry[e] = en;
     }
@@ -413,7 +455,7 @@ struct Routing {
 // ------------------------------------------------------------------- kernel 1: gate and up
 
 constexpr int kMaxPerWave = 4;  // steps of K a wave holds
-constexpr int kBatch = 16;      // items between two barriers
+constexpr int kBatch = 8;       // items between two barriers
 
 constexpr int kRedBytes = kBatch * kWaves * 64 * 16;
 
@@ -421,17 +463,17 @@ constexpr int kRedBytes = kBatch * kWaves * 64 * 16;
 // blocks' groups of `ways` waves, each with kSteps consecutive steps of K. Their scales come in
 // one load of 16 bytes per row and step (a load per step would have every wave fetch the
 // 128-byte line that holds a row's scales of 2048 k, as many bytes into the CU as the weights). The
-// partial sums of 16 items per group go to LDS before the waves meet at a barrier, then each
+// partial sums of 8 items per group go to LDS before the waves meet at a barrier, then each
 // wave finishes its items of them (finishing every item behind a barrier of its own left 7
 // waves waiting for the eighth: 3.0 us an item at K 6144).
 // kRoute: logits per lane of the router, 0 where the routing is given.
 // kTail: hidden is no multiple of 256.
 template <int kSteps, int kRoute, bool kTail>
 __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewArgs p, int ways) {
-  static_assert(kRedBytes + Routing::bytes(kMaxIds, kTable, kMaxRows) + 64 <= 160 * 1024, "LDS");
+  static_assert(kRedBytes + Routing::bytes(kMaxIds, kTable, kMaxRows) + 512 <= 160 * 1024, "LDS");
   constexpr int kDepth = kSteps <= 2 ? 4 : 2;  // items in flight
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-  __shared__ uint32_t s_top[16];
+  __shared__ uint32_t s_top[kWaves][16];  // largest magnitude of a wave's share of a row
   f32x4_t *red = reinterpret_cast<f32x4_t *>(dyn);  // [kBatch][kWaves][64]
   const int n_ids = p.rows * p.top_k;
   Routing rt(dyn + kRedBytes, n_ids, p.num_experts);
@@ -462,20 +504,24 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewArgs p, int
   __builtin_amdgcn_sched_barrier(0);
   const __amdgpu_buffer_rsrc_t x_rsrc =
       make_rsrc(p.x, static_cast<uint32_t>((p.rows - 1) * p.ld_x + p.hidden) * 2u);
-  u32x4_t xr[kSteps][8];
+  u32x4_t xr[kSteps][8];  // 16 bytes of row 2 q + lane / 32 per load: whole lines
   uint32_t w_voff[kSteps];
   const uint32_t row_bytes = static_cast<uint32_t>(p.hidden) / 2;
   const uint32_t srow_bytes = static_cast<uint32_t>(p.hidden) / 16;
   const uint32_t w_row = static_cast<uint32_t>((r16 & 7) + (r16 >= 8 ? p.mi : 0));
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
-    const int k = (kw * kSteps + i) * kStepK + 64 * kb;
-    const bool in = k < p.hidden;  // hidden is a multiple of 64
-    const uint32_t off = static_cast<uint32_t>(r16 * p.ld_x + k) * 2u;
+    const int k0 = (kw * kSteps + i) * kStepK, k = k0 + 64 * kb, xk = k0 + 8 * (lane & 31);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      xr[i][j] = load16(x_rsrc, in && r16 < p.rows ? off + 16 * j : kNoLoad, 0);
-    w_voff[i] = in ? w_row * row_bytes + static_cast<uint32_t>(k) / 2 : kNoLoad;
+    for (int q = 0; q < 8; ++q) {
+      const int row = 2 * q + (lane >> 5);
+      xr[i][q] = u32x4_t{0u, 0u, 0u, 0u};
+      if (2 * q < p.rows)  // wave-uniform
+        xr[i][q] = load16(x_rsrc, row < p.rows && xk < p.hidden
+                                      ? static_cast<uint32_t>(row * p.ld_x + xk) * 2u
+                                      : kNoLoad, 0);
+    }
+    w_voff[i] = k < p.hidden ? w_row * row_bytes + static_cast<uint32_t>(k) / 2 : kNoLoad;
   }
   // Lane kb loads the scales of step kb.
   const int s_k = (kw * kSteps + kb) * kStepK;
@@ -484,7 +530,6 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewArgs p, int
                               : kNoLoad;
 
   // 2. The routing, and each row's largest magnitude.
-  if (tid < 16) s_top[tid] = 0;
   if (kRoute > 0) {
 #pragma unroll
     for (int r = 0; r < kRouted; ++r) {
@@ -505,21 +550,40 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewArgs p, int
     rt.id[tid] = given;
   }
   rt.begin<kMaxRows>(p, fetched, tid);
-  __syncthreads();
-  rt.group<kMaxRows>(p, p.gate_up, tid);
-  {
+  // This wave's share of the rows goes through its piece of LDS (the place of the partial sums)
+  // into the order of the matrix instruction: x[i][j] is k 64 kb + 8 j of step i of row r16. Piece
+  // c of a row lies at c ^ (row % 8). With it, the rows' largest magnitudes.
+  const auto arrange = [&]() __attribute__((always_inline)) {
     typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    u32x4_t *mine = reinterpret_cast<u32x4_t *>(dyn) + wave * (16 * 32);
     u16x2_t m = {0, 0};
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
+    for (int i = 0; i < kSteps; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int q = 0; q < 8; ++q) {
+        const int row = 2 * q + (lane >> 5);
+        if (2 * q < p.rows) mine[row * 32 + ((lane & 31) ^ (row & 7))] = xr[i][q];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u32x4_t v = {0u, 0u, 0u, 0u};
+        if (r16 < p.rows) v = mine[r16 * 32 + ((8 * kb + j) ^ (r16 & 7))];
+        xr[i][j] = v;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          m = __builtin_elementwise_max(
-              m, __builtin_bit_cast(u16x2_t, xr[i][j][u] & 0x7FFF7FFFu));
-    atomicMax(&s_top[r16], static_cast<uint32_t>(max(m[0], m[1])));  // a maximum has no order
-  }
+          m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, v[u] & 0x7FFF7FFFu));
+      }
+    }
+    uint32_t top = max(m[0], m[1]);
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 16, 64)));
+    top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), 32, 64)));
+    if (kb == 0) s_top[wave][r16] = top;
+  };
+  // The first wave, which routes when there is one row, arranges while the last one groups.
+  if (wave != 0) arrange();
+  __syncthreads();
+  rt.group<kMaxRows>(p, p.gate_up, tid);
+  if (wave == 0) arrange();
   __syncthreads();
 
   // 3. Items and the first loads.
@@ -567,7 +631,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewArgs p, int
   }
 
   // 4. The rows as FP16, each brought to its largest magnitude's power of two.
-  const int shift = shift_of(static_cast<int>(s_top[r16] >> 7));
+  uint32_t top = 0;
+  for (int w = 0; w < ways; ++w) top = max(top, s_top[group * ways + w][r16]);
+  const int shift = shift_of(static_cast<int>(top >> 7));
   f16x8_t x[kSteps][8];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i)

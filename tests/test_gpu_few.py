@@ -113,7 +113,8 @@ def test_layer(hip, rows, e, hidden, mi, top_k):
 
 
 @pytest.mark.parametrize("rows,top_k,e", [(3, 4, 8), (8, 8, 8), (16, 8, 8), (16, 16, 20), (1, 64, 64),
-                                          (1, 200, 256), (2, 128, 300), (12, 8, 2)])
+                                          (1, 200, 256), (2, 128, 300), (12, 8, 2), (16, 5, 7),
+                                          (16, 8, 600), (9, 20, 513), (2, 40, 512)])
 def test_many_rows_per_expert_and_many_slots(hip, rows, top_k, e):
     """Every number of rows an expert can have, entries swept more than once, over 64 slots."""
     layer = Layer(hip, e, 256, 128, rows + top_k)
