@@ -944,14 +944,12 @@ def moe_w8a8_grouped_gemm_swiglu(a, a_scale, table: "Fp8ExpertTable", expert_off
         _p(act_scale), ld_os, rows, mi, table.k, float(limit), wp, wb, handle))
 
 
-def _like_rows(t, rows, cols, name):
-    """(tensor, leading dimension) of an optional BF16 [rows, cols] device tensor."""
-    if t is None:
-        return None, 0
+def _like_rows(t, shape, name):
+    """Leading dimension of a BF16 device tensor of the given shape."""
     t, ld = _bf16_matrix(t, name)
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name}: expected [{rows}, {cols}], got {tuple(t.shape)}")
-    return t, _one_row(cols) if rows <= 1 else ld
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected {list(shape)}, got {list(t.shape)}")
+    return _one_row(shape[1]) if shape[0] <= 1 else ld
 
 
 def _norm_rows(x, weight, residual, h, y):
@@ -959,15 +957,17 @@ def _norm_rows(x, weight, residual, h, y):
     import torch
 
     x, ld_x = _bf16_matrix(x, "x")
-    rows, cols = x.shape
+    shape = x.shape
+    rows, cols = shape
     if rows > _INT32_MAX or cols > _INT32_MAX:
         _no_int32(rows, cols)
-    if weight.dtype != torch.bfloat16 or weight.shape != (cols,) or not weight.is_contiguous():
+    if (weight.dtype != torch.bfloat16 or weight.dim() != 1 or weight.numel() != cols or
+            not weight.is_contiguous()):
         raise ValueError(f"weight: expected {cols} contiguous BF16 values")
-    ld_r = _like_rows(residual, rows, cols, "residual")[1]
-    ld_h = _like_rows(h, rows, cols, "h")[1]
-    ld_y = _like_rows(y, rows, cols, "y")[1]
-    return rows, cols, _one_row(cols) if rows <= 1 else ld_x, ld_r, ld_h, ld_y
+    ld_r = 0 if residual is None else _like_rows(residual, shape, "residual")
+    ld_h = 0 if h is None else _like_rows(h, shape, "h")
+    ld_y = 0 if y is None else _like_rows(y, shape, "y")
+    return shape, _one_row(cols) if rows <= 1 else ld_x, ld_r, ld_h, ld_y
 
 
 def moe_rmsnorm_bf16(x, weight, y, eps: float = 1e-6, residual=None, h=None,
@@ -975,7 +975,8 @@ def moe_rmsnorm_bf16(x, weight, y, eps: float = 1e-6, residual=None, h=None,
     """``h = bf16(x + residual)`` and ``y = bf16(h * weight / sqrt(mean(h^2) + eps))`` over BF16
     ``[rows, cols]`` views; ``h`` (the new residual stream, where given) may be ``x`` or
     ``residual``, ``y`` may be ``x``."""
-    rows, cols, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
+    shape, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
+    rows, cols = shape
     if y is None:
         raise TypeError("y: expected a BF16 tensor")
     handle = _launch_stream(stream, x, weight, residual, h, y)
@@ -990,10 +991,11 @@ def moe_rmsnorm_fp8(x, weight, q, scale, eps: float = 1e-6, residual=None, h=Non
                     stream=None) -> None:
     """moe_rmsnorm_bf16 with its rows quantised, as moe_quant_fp8 does, from the unrounded norm:
     E4M3 ``q [rows, cols]``, ``scale [rows, ceil(cols / 128)]``; ``y`` too where given."""
-    rows, cols, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
+    shape, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
+    rows, cols = shape
     ld_q = _fp8_matrix(q, "q")
-    if q.shape != x.shape:
-        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
+    if q.shape != shape:
+        raise ValueError(f"shape mismatch: x {tuple(shape)}, q {tuple(q.shape)}")
     if rows <= 1:
         ld_q = _one_row(cols)
     ld_s = _scale_matrix(scale, rows, _fp8_blocks(cols), "scale")
@@ -1021,9 +1023,9 @@ def _scale_vector(t, n, name):
     """Checks a contiguous float32 device vector of at least n scales."""
     import torch
 
-    if t.dtype != torch.float32 or len(t.shape) != 1 or not t.is_cuda:
+    if t.dtype != torch.float32 or t.dim() != 1 or not t.is_cuda:
         raise TypeError(f"{name}: expected a 1-D float32 device tensor")
-    if t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+    if t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name}: needs {n} contiguous scales")
 
 
@@ -1031,10 +1033,11 @@ def moe_rmsnorm_int8(x, weight, q, scale, eps: float = 1e-6, residual=None, h=No
                      stream=None) -> None:
     """moe_rmsnorm_bf16 with its rows quantised, as moe_quant_int8 does, from the unrounded norm:
     INT8 ``q [rows, cols]``, ``scale [rows]``; ``y`` too where given."""
-    rows, cols, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
+    shape, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
+    rows, cols = shape
     ld_q = _int8_matrix(q, "q")
-    if q.shape != x.shape:
-        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, q {tuple(q.shape)}")
+    if q.shape != shape:
+        raise ValueError(f"shape mismatch: x {tuple(shape)}, q {tuple(q.shape)}")
     if rows <= 1:
         ld_q = _one_row(cols)
     _scale_vector(scale, rows, "scale")
@@ -1192,6 +1195,8 @@ class SharedExpertInt8:
         inter, hidden = gate_w.shape
         if tuple(up_w.shape) != (inter, hidden) or tuple(down_w.shape) != (hidden, inter):
             raise ValueError("expected gate_w, up_w [I, H] and down_w [H, I]")
+        if inter > _INT32_MAX or hidden > _INT32_MAX or max_rows > _INT32_MAX:
+            _no_int32(inter, hidden, max_rows)
         self.ld_w, self.ld_down = _int8_matrix(gate_w, "gate_w"), _int8_matrix(down_w, "down_w")
         if _int8_matrix(up_w, "up_w") != self.ld_w:
             raise ValueError("gate_w and up_w must have the same strides")
@@ -1436,6 +1441,8 @@ class FewWorkspace:
 
         if not 1 <= max_rows <= FEW_MAX_ROWS or not 1 <= top_k <= FEW_MAX_IDS // max_rows:
             raise ValueError("the few-token layer takes 1..16 rows and rows * top_k <= 256")
+        if moe_intermediate > _INT32_MAX:
+            _no_int32(moe_intermediate)
         self.max_rows, self.top_k = max_rows, top_k
         self.moe_intermediate = moe_intermediate
         need = int(load().moe_few_workspace_bytes(max_rows, top_k, moe_intermediate))
@@ -1470,12 +1477,13 @@ def _layer_few(x, logits, bias, routed_scale, renormalize, topk_ids, topk_weight
             raise ValueError(f"shared must be [{rows}, {hidden}]")
     if rows <= 1:
         ld_x = ld_out = ld_s = _one_row(hidden)
+    ld_l = 0 if logits is None else logits.stride(0) if rows > 1 else logits.shape[1]
     _check("moe_w4a16_layer_few", load().moe_w4a16_layer_few(
-        _p(x), ld_x, _p(logits), 0 if logits is None else max(logits.stride(0), logits.shape[1]),
-        _p(bias), float(routed_scale), 1 if renormalize else 0, _p(topk_ids), _p(topk_weights),
-        _p(gate_up.packed_ptrs), _p(gate_up.scale_ptrs), _p(gate_up.scale2), _p(down.packed_ptrs),
-        _p(down.scale_ptrs), _p(down.scale2), gate_up.num_experts, _p(shared), ld_s, _p(out),
-        ld_out, rows, top_k, hidden, mi, float(limit), _p(ws.buffer), ws.buffer.numel(), handle))
+        _p(x), ld_x, _p(logits), ld_l, _p(bias), float(routed_scale), 1 if renormalize else 0,
+        _p(topk_ids), _p(topk_weights), _p(gate_up.packed_ptrs), _p(gate_up.scale_ptrs),
+        _p(gate_up.scale2), _p(down.packed_ptrs), _p(down.scale_ptrs), _p(down.scale2),
+        gate_up.num_experts, _p(shared), ld_s, _p(out), ld_out, rows, top_k, hidden, mi,
+        float(limit), _p(ws.buffer), ws.buffer.numel(), handle))
 
 
 def moe_layer_few(x, topk_ids, topk_weights, gate_up: ExpertTable, down: ExpertTable,
@@ -1483,8 +1491,8 @@ def moe_layer_few(x, topk_ids, topk_weights, gate_up: ExpertTable, down: ExpertT
     """The routed layer for 1..16 rows in two kernels: gate_up with the SwiGLU clamp over the
     union of the rows' experts, then down, the weighted sum and the shared term. Weights are
     decoded to FP16 exactly, ``scale2`` multiplies the FP32 sums, and only the SwiGLU's output
-    is rounded to BF16 on the way, so outputs are nearer to the formula than ``moe_layer`` and
-    ``moe_layer_decode``, and not the same bits. ``shared`` is a BF16 ``[rows, H]`` tensor, a
+    is rounded on the way (to FP16 up to a ``limit`` of 128, else to BF16), so outputs are nearer
+    to the formula than ``moe_layer`` and ``moe_layer_decode``, and not the same bits. ``shared`` is a BF16 ``[rows, H]`` tensor, a
     ``SharedExpert`` or a ``SharedExpertInt8`` (run over ``x`` first)."""
     import torch
 
@@ -1512,6 +1520,8 @@ def moe_layer_few_from_logits(x, logits, top_k: int, gate_up: ExpertTable, down:
     rows, n_exp = x.shape[0], gate_up.num_experts
     if logits.shape != (rows, n_exp) or (n_exp > 1 and logits.stride(1) != 1):
         raise ValueError(f"logits: expected [{rows}, {n_exp}], rows contiguous")
+    if rows > 1 and logits.stride(0) < n_exp:
+        raise ValueError("logits: the rows overlap")
     _want(topk_ids, torch.int32, "topk_ids")
     _want(topk_weights, torch.float32, "topk_weights")
     for t, name in ((topk_ids, "topk_ids"), (topk_weights, "topk_weights")):
