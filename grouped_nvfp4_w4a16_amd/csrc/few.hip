@@ -1,7 +1,7 @@
 // moe_w4a16_layer_few: a whole routed NVFP4 layer for at most 16 tokens in two kernels.
 //
 //   kernel 1   router (logits -> top-k), the rows' experts, gate_up + SwiGLU:
-//              act[slot] = bf16( swiglu( s2_e sum_k x[r, k] w_e[:, k] ) )
+//              act[slot] = fp16 or bf16( swiglu( s2_e sum_k x[r, k] w_e[:, k] ) )
 //   kernel 2   down, the weighted sum over a row's slots and the shared term:
 //              out[r] = bf16( sum_slot (p_slot s2_e) sum_k act[slot, k] w_e[:, k] + shared[r] )
 //
@@ -455,9 +455,12 @@ struct Routing {
 // ------------------------------------------------------------------- kernel 1: gate and up
 
 constexpr int kMaxPerWave = 4;  // steps of K a wave holds
-constexpr int kBatch = 8;       // items between two barriers
-
+// Items between two barriers. Past-the-end ones cost about 0.5 us each: with 16 of them one token's
+// layer took 4 us more.
+constexpr int kBatch = 8;
 constexpr int kRedBytes = kBatch * kWaves * 64 * 16;
+constexpr int kArrangeBytes = kWaves * 16 * 32 * 16;  // a step of every wave's share of 16 rows
+static_assert(kArrangeBytes <= kRedBytes, "the rows are arranged where the partial sums go later");
 
 // An item is 8 gate rows and the same 8 up rows of one entry. Items are dealt round-robin to the
 // blocks' groups of `ways` waves, each with kSteps consecutive steps of K. Their scales come in
@@ -555,7 +558,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewArgs p, int
   // c of a row lies at c ^ (row % 8). With it, the rows' largest magnitudes.
   const auto arrange = [&]() __attribute__((always_inline)) {
     typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
-    u32x4_t *mine = reinterpret_cast<u32x4_t *>(dyn) + wave * (16 * 32);
+    u32x4_t *mine = reinterpret_cast<u32x4_t *>(dyn) + wave * (16 * 32);  // kArrangeBytes in all
     u16x2_t m = {0, 0};
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
@@ -600,7 +603,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewArgs p, int
   const uint32_t s_total = 2u * static_cast<uint32_t>(p.mi) * srow_bytes;
   // The item whose loads come next: its number, entry and tile.
   int next = first + group, next_e = next / tiles, next_t = next - next_e * tiles;
-  const auto load_w = [&](Loads &l, const Entry &en, bool in, int i) __attribute__((always_inline)) {
+  const auto load_w = [&](Loads &l, const Entry &en, bool in, int i)
+      __attribute__((always_inline)) {
     const __amdgpu_buffer_rsrc_t wr = make_rsrc(rfl_ptr(en.packed), in ? w_total : 0u);
     const uint32_t row = static_cast<uint32_t>(next_t) * 8u;
     l.w[i][0] = load16(wr, w_voff[i], row * row_bytes);
@@ -650,7 +654,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_gate_up_kernel(FewArgs p, int
     float o[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float v = __builtin_amdgcn_ldexpf(sum[u], -shift) * s2;  // gate or up, tile row 4 kb + u
+      // gate or up, tile row 4 kb + u
+      const float v = __builtin_amdgcn_ldexpf(sum[u], -shift) * s2;
       o[u] = moe::fp8_swiglu(v, __shfl_xor(v, 32, 64), p.limit);
     }
     const int slot = rt.slot_of[e * 16 + r16];
@@ -957,7 +962,8 @@ int launch_gate_up(const FewArgs &p, void *stream) {
   const int lds = kRedBytes + Routing::bytes(p.rows * p.top_k, p.num_experts, kMaxRows);
   const auto go = [&](auto kern) -> int {
     constexpr auto k = decltype(kern)::value;
-    MOE_REQUIRE_CODE(moe::allow_lds<k>(kRedBytes + Routing::bytes(kMaxIds, kTable, kMaxRows)), MOE_ELAUNCH, "layer_few: LDS was refused");
+    MOE_REQUIRE_CODE(moe::allow_lds<k>(kRedBytes + Routing::bytes(kMaxIds, kTable, kMaxRows)),
+                     MOE_ELAUNCH, "layer_few: LDS was refused");
     return moe::launch("moe_w4a16_layer_few", k, dim3(static_cast<unsigned>(blocks)),
                        dim3(kThreads), static_cast<size_t>(lds), stream, p, s.ways);
   };
@@ -995,13 +1001,20 @@ int launch_down(const FewArgs &p, void *stream) {
   const auto go = [&](auto kern, int cap) -> int {
     constexpr auto k = decltype(kern)::value;
     const int lds = down_lds(ids, p.num_experts, cap);
-    MOE_REQUIRE_CODE(moe::allow_lds<k>(down_lds(kMaxIds, kTable, 8)), MOE_ELAUNCH, "layer_few: LDS was refused");
+    MOE_REQUIRE_CODE(moe::allow_lds<k>(down_lds(kMaxIds, kTable, 8)), MOE_ELAUNCH,
+                     "layer_few: LDS was refused");
     return moe::launch("moe_w4a16_layer_few", k, grid, dim3(kThreads), static_cast<size_t>(lds),
                        stream, p);
   };
-  // Rows staged at a time, by how many an expert has on average over all experts.
-  if (2 * ids <= p.num_experts || p.rows <= 2) return go(Kern<few_down_kernel<2, kHalf, kTail>>{}, 2);
-  if (ids <= 2 * p.num_experts || p.rows <= 4) return go(Kern<few_down_kernel<4, kHalf, kTail>>{}, 4);
+  // Rows staged at a time, by how many an expert has on average over all experts: an expert with
+  // more is swept again, empty rows cost registers (fewer blocks per CU) and loads. us of the whole
+  // layer for 2 / 4 / 8 rows: 8 rows of 8 among 256 experts 233.6 / 236.1 / 258.1, 16 rows of 8
+  // among 64 54.8 / 51.4 / 54.5, 16 rows of 2 among 8 53.2 / 47.6 / 49.6, 16 rows of 8 among 8
+  // (4 / 8 rows) 78.6 / 69.0.
+  if (2 * ids <= p.num_experts || p.rows <= 2)
+    return go(Kern<few_down_kernel<2, kHalf, kTail>>{}, 2);
+  if (ids <= 4 * p.num_experts || p.rows <= 4)
+    return go(Kern<few_down_kernel<4, kHalf, kTail>>{}, 4);
   return go(Kern<few_down_kernel<8, kHalf, kTail>>{}, 8);
 }
 

@@ -539,7 +539,8 @@ int launch_tile(const char *name, const GemmArgs &p, void *stream) {
   MOE_REQUIRE(tiles < (1ll << 32) / C::kThreads, "%s: matrix too large", name);
   constexpr auto kern = tile_kernel<C, kSwiglu>;
   if (C::kLds > 64 * 1024)
-    MOE_REQUIRE_CODE(moe::allow_lds<kern>(C::kLds), MOE_ELAUNCH, "%s: %d bytes of LDS were refused", name,
+    MOE_REQUIRE_CODE(moe::allow_lds<kern>(C::kLds), MOE_ELAUNCH,
+                     "%s: %d bytes of LDS were refused", name,
                    C::kLds);
   return moe::launch(name, kern, dim3(static_cast<unsigned>(tiles)), dim3(C::kThreads), C::kLds,
                      stream, p);
@@ -611,7 +612,8 @@ extern "C" int moe_dense_gemm_int8(const int8_t *a, int64_t lda, const float *a_
                                    uint16_t *c, int64_t ldc, int32_t m, int32_t n, int32_t k,
                                    void *stream) {
   moe::clear_error();
-  const GemmArgs p = {a, a_scale, b, nullptr, b_scale, nullptr, c, nullptr, lda, ldb, ldc, m, n, k, 0.0f};
+  const GemmArgs p = {a,   a_scale, b,   nullptr, b_scale, nullptr, c,   nullptr,
+                      lda, ldb,     ldc, m,       n,       k,       0.0f};
   const int rc = check_gemm("dense_gemm_int8", p, false);
   if (rc != MOE_OK || m == 0) return rc;
   return launch_gemm<false>("moe_dense_gemm_int8", p, stream);

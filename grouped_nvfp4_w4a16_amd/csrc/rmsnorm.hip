@@ -207,7 +207,8 @@ __global__ __launch_bounds__(kMaxThreads) void norm_kernel(NormArgs p) {
     }
     if constexpr (kNorm)
       if (live && p.h != nullptr) *reinterpret_cast<uint4 *>(p.h + row * p.ld_h + col) = v.v;
-    if (kNorm && live && p.y != nullptr) *reinterpret_cast<uint4 *>(p.y + row * p.ld_y + col) = pack8(f);
+    if (kNorm && live && p.y != nullptr)
+      *reinterpret_cast<uint4 *>(p.y + row * p.ld_y + col) = pack8(f);
     if (kOut == Out::kFp8) {
       uint32_t m = 0;
 #pragma unroll
