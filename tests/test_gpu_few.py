@@ -315,6 +315,45 @@ def test_captured_replayed_and_on_two_streams(hip, rows, e):
     assert torch.equal(oa, eager) and torch.equal(ob, eager)
 
 
+@pytest.mark.parametrize("rows,e,top_k", [(16, 24, 8), (13, 600, 5), (7, 40, 9)])
+def test_repeated_and_replayed_calls_and_slots_in_another_order(hip, rows, e, top_k):
+    """Slots grouped by every path (a wave's ballots, masks, the scan): repeated calls give the same
+    bits, in a replayed graph too; slots in another order stay within the bounds."""
+    layer = Layer(hip, min(e, 24), 512, 192, rows)
+    pick = np.random.default_rng(e).integers(0, layer.e, e)
+    layer.gu, layer.dn = [layer.gu[i] for i in pick], [layer.dn[i] for i in pick]
+    layer.s1, layer.s2, layer.e = layer.s1[pick], layer.s2[pick], e
+    layer.tables(hip)
+    x, ids, w = layer.inputs(rows, top_k)
+    xd, idd, wd = bf16_dev(x), dev(ids), dev(w)
+    ws, out = hip.FewWorkspace(rows, top_k, 192), torch.empty(rows, 512, dtype=BF16, device="cuda")
+
+    def call(o):
+        hip.moe_layer_few(xd, idd, wd, layer.gt, layer.dt, 7.0, ws, o)
+
+    call(out)
+    first = out.clone()
+    ref, terms = layer.oracle(x, ids, w)
+    _check(f64(first), ref, terms, 512)
+    for _ in range(5):
+        call(out)
+        assert torch.equal(out, first)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    idd.copy_(dev(ids[:, ::-1].copy()))
+    wd.copy_(dev(w[:, ::-1].copy()))
+    graph.replay()
+    torch.cuda.synchronize()
+    _check(f64(out), ref, terms, 512)
+
+
 def test_a_layer_in_the_order_it_is_used(hip):
     """Norm with the residual, router logits, INT8 shared expert, few-token layer: two layers in a
     row through one residual stream, captured, against the same calls with separate pieces."""
