@@ -1111,12 +1111,14 @@ extern "C" int moe_w4a16_layer_few(
   p.routed_scale = routed_scale;
   p.limit = limit;
   p.tile_rows = tile_rows_of(hidden);
-  // |act| <= limit^2: FP16 holds it with 11 bits wherever it is above limit^2 2^-30. A wider
-  // limit leaves it in BF16, with a power of two per slot.
+  // |act| <= limit max(limit, 0.2785): the gate is clamped from above only, and silu's least value
+  // is -0.27846. The power of two that brings this bound to [2^14, 2^15) leaves FP16 its 11 bits
+  // down to 2^-28 of it. A wider limit leaves activations in BF16, with a power of two per slot.
   p.act_half = limit <= kHalfLimit;
   if (p.act_half) {
+    const double l = limit;
     int exponent;
-    std::frexp(static_cast<double>(limit) * limit, &exponent);  // limit^2 < 2^exponent
+    std::frexp(l * std::max(l, 0.2785), &exponent);  // the bound is below 2^exponent
     p.act_shift = std::min(15 - exponent, 120);
   }
   const bool in_kernel = logits != nullptr && num_experts <= kRouterExperts;
