@@ -1490,9 +1490,11 @@ def moe_layer_few(x, topk_ids, topk_weights, gate_up: ExpertTable, down: ExpertT
                   limit: float, ws: FewWorkspace, out, shared=None, stream=None) -> None:
     """The routed layer for 1..16 rows in two kernels: gate_up with the SwiGLU clamp over the
     union of the rows' experts, then down, the weighted sum and the shared term. Weights are
-    decoded to FP16 exactly, ``scale2`` multiplies the FP32 sums, and only the SwiGLU's output
-    is rounded on the way (to FP16 up to a ``limit`` of 128, else to BF16), so outputs are nearer
-    to the formula than ``moe_layer`` and ``moe_layer_decode``, and not the same bits. ``shared`` is a BF16 ``[rows, H]`` tensor, a
+    decoded to FP16 exactly and ``scale2`` multiplies the FP32 sums. Rows are held in FP16 times a
+    power of two (exact down to 2^-31 of a row's largest value, see the header), and the SwiGLU's
+    output is rounded (to FP16 up to a ``limit`` of 128, else to BF16): outputs are nearer to the
+    formula than those of ``moe_layer`` and ``moe_layer_decode``, unless a row's values spread wider,
+    and not the same bits. ``shared`` is a BF16 ``[rows, H]`` tensor, a
     ``SharedExpert`` or a ``SharedExpertInt8`` (run over ``x`` first)."""
     import torch
 

@@ -18,8 +18,10 @@
 //     the weight, takes 14 operations per 8 weights and a table lookup in LDS per 16). scale2 is
 //     applied to the FP32 sums. The matrix instruction is v_mfma_f32_16x16x32_f16.
 //   - So activations are FP16 too. BF16 values times a power of two per row (that brings the
-//     row's largest magnitude to [2^14, 2^15)) are exact in FP16 down to 2^-28 of the largest;
-//     below, they are off by at most 2^-39 of it, far below what FP32 sums keep.
+//     row's largest magnitude to [2^14, 2^15)) are exact in FP16 down to 2^-31 of the largest;
+//     below, they are cut to multiples of 2^-24 there and off by less than 2^-38 of it. Beside the
+//     largest value's own product that is far below what FP32 sums keep; where that one's weight
+//     is zero it is what is left of the sum (moe_layer and moe_layer_decode keep BF16 rows).
 //   - Kernel 1 holds its K share of all rows' activations in registers for its whole life: a wave
 //     takes the same 256-k steps of every item, so nothing but weights is loaded in its loop.
 //     Two items are in flight per wave (110 KB per CU at K 6144).

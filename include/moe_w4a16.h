@@ -852,14 +852,17 @@ int64_t moe_shared_expert_int8_workspace_bytes(int32_t m, int32_t inter);
  * kernels: the router (optional), gate_up with the clamped SwiGLU, down, the weighted sum over
  * a row's slots and the shared term:
  *
- *   G, U        = (sum_k x[r, k] q[n, k] d[n, k / 16]) * gate_up_scale2[e]
+ *   G, U        = (sum_k f(x[r, k]) q[n, k] d[n, k / 16]) * gate_up_scale2[e]
  *   act[slot]   = r( silu(min(G, limit)) * clamp(U, -limit, limit) )
  *   out[r, h]   = bf16( sum_slot topk_weights[slot] * down_scale2[e] *
  *                       (sum_k act[slot, k] q[h, k] d[h, k / 16])  + shared[r, h] )
  *
  * with q the E2M1 value and d the E4M3 block scale of a weight (tables as in
- * moe_w4a16_grouped_gemm and its SwiGLU form) and r the rounding to FP16 times a power of two
- * (11 bits; limit <= 128) or to BF16 (a wider limit). A weight is the exact product q d; unlike the
+ * moe_w4a16_grouped_gemm and its SwiGLU form). f is FP16 times a power of two per row: x itself down
+ * to 2^-31 of the row's largest magnitude, below that cut by less than 2^-38 of it (a row whose
+ * values spread wider holds fewer bits of its smallest than in the other calls). r is the rounding to
+ * FP16 times a power of two (limit <= 128: 11 bits down to 2^-28 of limit * max(limit, 0.2785), which
+ * no activation exceeds) or to BF16 (a wider limit). A weight is the exact product q d; unlike the
  * other calls, scale2 multiplies the FP32 sums and is not rounded into a BF16 weight, and the
  * gate_up values and the experts' outputs are not rounded to BF16 on the way. Sums are FP32, in
  * a fixed order for given inputs that depends on the experts of all rows.

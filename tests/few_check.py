@@ -23,11 +23,12 @@ def signs(rng, rows, hidden):
     return (v.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
 
 
-def assert_exact(gate_up, rows):
-    """The magnitudes of every sum of these rows (FP64) stay below 2^16."""
+def assert_exact(gate_up, rows, step=1.0):
+    """The magnitudes of every sum of these rows (FP64, multiples of `step`) stay below 2^16 step."""
+    assert np.array_equal(np.rint(rows / step) * step, rows)
     most = np.abs(rows).max(axis=0)
     for w in gate_up:
-        assert w is None or (np.abs(ffn.code_values(*w)) @ most).max() < 2.0 ** 16
+        assert w is None or (np.abs(ffn.code_values(*w)) @ most).max() < 2.0 ** 16 * step
 
 
 def bounds(ref, terms, limit):

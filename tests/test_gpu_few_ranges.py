@@ -26,3 +26,55 @@ def test_small_limits(hip, limit, rows, e):
     got = f64(_run(hip, layer, bf16_dev(x), ids, w, limit))
     elem = bounds(ref, terms, limit)
     assert np.all(np.abs(got - ref) <= elem), float(np.max(np.abs(got - ref) / elem))
+
+
+def _without_channel(layer, k):
+    """The layer with zero gate and up weights for channel k."""
+    for packed, _ in layer.gu:
+        packed[:, k // 2] &= 0xF0 if k % 2 == 0 else 0x0F
+
+
+@pytest.mark.parametrize("spread", [2.0 ** 20, 2.0 ** 31, 2.0 ** 36, 2.0 ** 38, 2.0 ** 39, 2.0 ** 44])
+@pytest.mark.parametrize("channel", [0, 301])
+def test_values_far_below_the_rows_largest(hip, spread, channel):
+    """A channel that all weights skip, `spread` times the other values (-1, 0, 1): these stay what they
+    are while they are multiples of 2^-38 of it, and become zeros below."""
+    layer = Layer(hip, 5, 512, 192, 9, mean=2.0)
+    _without_channel(layer, channel)
+    layer.tables(hip)
+    _, ids, w = layer.inputs(6, 3)
+    x = signs(layer.rng, 6, 512)
+    x[:, channel] = 0
+    clean = _run(hip, layer, bf16_dev(x), ids, w)
+    ref, terms = layer.oracle(x, ids, w)
+    assert_exact(layer.gu, codecs.bf16_bits_to_f64(x))
+    assert np.all(np.abs(f64(clean) - ref) <= bounds(ref, terms, 7.0))
+    rows = [1, 3, 4]
+    x[rows, channel] = np.float32(spread).view(np.uint32) >> 16
+    got = _run(hip, layer, bf16_dev(x), ids, w)
+    gone = spread > 2.0 ** 38
+    keep = [r for r in range(6) if not gone or r not in rows]
+    assert np.array_equal(f64(got)[keep], f64(clean)[keep])
+    assert not gone or not np.any(f64(got)[rows])
+
+
+@pytest.mark.parametrize("spread,step", [(2.0 ** 35, 2.0 ** -3), (2.0 ** 38, 1.0)])
+def test_values_below_the_exact_ones_are_cut_as_stated(hip, spread, step):
+    """Values of 8 significant bits in [1, 2) below a skipped channel of `spread`: the layer's outputs are
+    those of the values cut towards zero to multiples of 2^-38 spread, bit for bit."""
+    layer = Layer(hip, 3, 256, 64, 13, mean=2.0)
+    _without_channel(layer, 5)
+    layer.tables(hip)
+    _, ids, w = layer.inputs(4, 2)
+    v = layer.rng.choice([-1.0, 1.0], (4, 256)) * (1 + layer.rng.integers(0, 128, (4, 256)) / 128)
+    v[:, 5] = spread
+    cut = np.trunc(v / step) * step
+    assert_exact(layer.gu, cut, step)
+
+    def bits(a):
+        return (a.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    got = _run(hip, layer, bf16_dev(bits(v)), ids, w)
+    want = _run(hip, layer, bf16_dev(bits(cut)), ids, w)
+    assert np.array_equal(f64(got), f64(want)) and np.any(f64(got))
+    ref, terms = layer.oracle(bits(cut), ids, w)
+    assert np.all(np.abs(f64(got) - ref) <= bounds(ref, terms, 7.0))
