@@ -42,6 +42,8 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kRowBytes = 128;  // one LDS row: 128 k
 constexpr int kMaxK = MOE_INT8_MAX_K;
+// Rows and output columns: rounded up to whole tiles (256 at most) they stay within 32 bits.
+constexpr int kMaxOut = 0x7FFFFFFF - 255;
 constexpr int kGroupM = 4;  // row tiles that run next to each other
 constexpr int kCus = 256;
 
@@ -588,6 +590,8 @@ int check_gemm(const char *name, const GemmArgs &p, bool swiglu) {
   MOE_REQUIRE(p.m >= 0 && p.n > 0 && p.n % 16 == 0 && p.k > 0 && p.k % 16 == 0 && p.k <= kMaxK,
               "%s: need m >= 0, n > 0 and k > 0 multiples of 16, k <= %d (m=%d n=%d k=%d)", name,
               kMaxK, p.m, p.n, p.k);
+  MOE_REQUIRE(p.m <= kMaxOut && p.n <= kMaxOut, "%s: at most %d rows and columns (m=%d n=%d)", name,
+              kMaxOut, p.m, p.n);
   MOE_REQUIRE(p.lda >= p.k && p.lda % 16 == 0 && p.ldw >= p.k && p.ldw % 16 == 0 &&
                   p.lda < (1 << 22) && p.ldw < (1 << 22),
               "%s: leading dimensions must be >= k, multiples of 16 and below 2^22", name);

@@ -792,9 +792,9 @@ int moe_quant_int8(const uint16_t *x, int64_t ld_x, int8_t *q, int64_t ld_q, flo
  *   b        int8 [n, ldb]  the weight, one row per output channel
  *   b_scale  float [n]
  *   c        bf16 [m, ldc]
- * Requirements (else MOE_EINVAL): m >= 0; n > 0 and k > 0 multiples of 16, k <= MOE_INT8_MAX_K;
- * lda >= k and ldb >= k, multiples of 16 below 2^22; ldc >= n and a multiple of 4; a and b
- * 16-byte, c 8-byte and the scales 4-byte aligned, all non-NULL when m > 0.
+ * Requirements (else MOE_EINVAL): m >= 0; n > 0 and k > 0 multiples of 16, k <= MOE_INT8_MAX_K; m and
+ * n at most 2^31 - 256; lda >= k and ldb >= k, multiples of 16 below 2^22; ldc >= n and a multiple
+ * of 4; a and b 16-byte, c 8-byte and the scales 4-byte aligned, all non-NULL when m > 0.
  */
 int moe_dense_gemm_int8(const int8_t *a, int64_t lda, const float *a_scale, const int8_t *b,
                         int64_t ldb, const float *b_scale, uint16_t *c, int64_t ldc, int32_t m,
