@@ -1032,7 +1032,8 @@ def _scale_vector(t, n, name):
 def moe_rmsnorm_int8(x, weight, q, scale, eps: float = 1e-6, residual=None, h=None, y=None,
                      stream=None) -> None:
     """moe_rmsnorm_bf16 with its rows quantised, as moe_quant_int8 does, from the unrounded norm:
-    INT8 ``q [rows, cols]``, ``scale [rows]``; ``y`` too where given."""
+    INT8 ``q [rows, cols]``, ``scale [rows]``; ``y`` too where given. Without columns nothing is
+    written, no scale either."""
     shape, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
     rows, cols = shape
     ld_q = _int8_matrix(q, "q")
@@ -1051,7 +1052,7 @@ def moe_rmsnorm_int8(x, weight, q, scale, eps: float = 1e-6, residual=None, h=No
 
 def moe_quant_int8(x, q, scale, stream=None) -> None:
     """Quantise BF16 rows ``x [rows, cols]`` to INT8 codes ``q [rows, cols]`` with one FP32 scale
-    per row, ``scale [rows]``; see the header."""
+    per row, ``scale [rows]``; see the header. Without columns nothing is written, no scale either."""
     x, ld_x = _bf16_matrix(x, "x")
     ld_q = _int8_matrix(q, "q")
     rows, cols = x.shape

@@ -750,7 +750,8 @@ int moe_w8a8_grouped_gemm_swiglu(const uint8_t *a, int64_t lda, const float *a_s
  * Requirements (else MOE_EINVAL): 0 <= rows < 2^22; cols >= 0, a multiple of 8; eps finite and
  * >= 0; leading dimensions >= cols and multiples of 8; ld_scale >= ceil(cols / 128); x,
  * residual, weight, h and y 16-byte aligned, q 8-byte, scale 4-byte; required pointers
- * non-NULL when rows * cols > 0.
+ * non-NULL when rows * cols > 0. Without rows or columns nothing is enqueued: no output is written,
+ * the INT8 form's scales of rows without columns included.
  */
 int moe_rmsnorm_bf16(const uint16_t *x, int64_t ld_x, const uint16_t *residual, int64_t ld_res,
                      const uint16_t *weight, float eps, uint16_t *h, int64_t ld_h, uint16_t *y,
@@ -771,7 +772,8 @@ int moe_rmsnorm_int8(const uint16_t *x, int64_t ld_x, const uint16_t *residual, 
  * with a NaN or an infinity gets a NaN or infinite scale and codes 0.
  *
  *   x bf16 [rows, ld_x], q int8 [rows, ld_q], scale float [rows]
- * Requirements (else MOE_EINVAL): those of moe_rmsnorm_int8 on x, q, scale, rows and cols.
+ * Requirements (else MOE_EINVAL): those of moe_rmsnorm_int8 on x, q, scale, rows and cols. As there,
+ * rows without columns get no scale.
  */
 int moe_quant_int8(const uint16_t *x, int64_t ld_x, int8_t *q, int64_t ld_q, float *scale,
                    int32_t rows, int32_t cols, void *stream);
