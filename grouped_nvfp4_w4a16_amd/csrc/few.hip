@@ -70,7 +70,7 @@ static_assert(kMaxIds <= kThreads, "one thread per slot");
 struct Tables {
   const uint64_t *packed, *scales;
   const float *scale2;
-  const uint64_t *other;  // the other projection's weights: an expert needs both
+  const uint64_t *other_packed, *other_scales;  // the other projection's: an expert needs both
 };
 
 struct FewArgs {
@@ -283,10 +283,11 @@ struct Entry {
 };
 
 __device__ __forceinline__ Entry entry_of(const Tables &t, int e) {
-  const uint64_t packed = t.packed[e], other = t.other[e], scales = t.scales[e];
-  const float scale2 = t.scale2[e];  // all four on their way before one is looked at
-  const bool both = (packed != 0) & (other != 0);
-  return {both ? packed : 0, scales, scale2, 0};
+  const uint64_t packed = t.packed[e], scales = t.scales[e];
+  const uint64_t other_packed = t.other_packed[e], other_scales = t.other_scales[e];
+  const float scale2 = t.scale2[e];  // all five on their way before one is looked at
+  const bool whole = (packed != 0) & (scales != 0) & (other_packed != 0) & (other_scales != 0);
+  return {whole ? packed : 0, scales, scale2, 0};
 }
 
 struct Routing {
@@ -1094,8 +1095,8 @@ extern "C" int moe_w4a16_layer_few(
   p.wts_out = topk_weights ? topk_weights : reinterpret_cast<float *>(ws + l.wts);
   p.ids = p.ids_out;
   p.wts = p.wts_out;
-  p.gate_up = {gate_up_packed, gate_up_scales, gate_up_scale2, down_packed};
-  p.down = {down_packed, down_scales, down_scale2, gate_up_packed};
+  p.gate_up = {gate_up_packed, gate_up_scales, gate_up_scale2, down_packed, down_scales};
+  p.down = {down_packed, down_scales, down_scale2, gate_up_packed, gate_up_scales};
   p.shared = shared;
   p.out = out;
   p.act = reinterpret_cast<uint16_t *>(ws);

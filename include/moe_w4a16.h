@@ -872,8 +872,8 @@ int64_t moe_shared_expert_int8_workspace_bytes(int32_t m, int32_t inter);
  * With logits, the routing is moe_router_topk's (its arguments; num_experts <=
  * MOE_ROUTER_MAX_EXPERTS, top_k <= MOE_ROUTER_MAX_TOPK; above 512 experts the router is a launch
  * of its own) and is written to topk_ids and topk_weights where they are given; without, they
- * are read. A slot whose id is outside [0, num_experts), whose expert has a null entry in one of
- * the tables, or that repeats an id of its row adds nothing.
+ * are read. A slot whose id is outside [0, num_experts), whose expert has a null address in one of
+ * the four tables of weights and scales, or that repeats an id of its row adds nothing.
  *
  *   x             bf16 [rows, ld_x]
  *   logits        float [rows, ld_logits] or NULL;  bias float [num_experts] or NULL

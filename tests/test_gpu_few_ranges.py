@@ -78,3 +78,26 @@ def test_values_below_the_exact_ones_are_cut_as_stated(hip, spread, step):
     assert np.array_equal(f64(got), f64(want)) and np.any(f64(got))
     ref, terms = layer.oracle(bits(cut), ids, w)
     assert np.all(np.abs(f64(got) - ref) <= bounds(ref, terms, 7.0))
+
+
+@pytest.mark.parametrize("table", ["gt", "dt"])
+@pytest.mark.parametrize("field", ["packed_ptrs", "scale_ptrs"])
+@pytest.mark.parametrize("rows,e,top_k", [(3, 6, 3), (16, 9, 6), (13, 520, 6)])
+def test_an_expert_with_a_null_address_in_one_table(hip, table, field, rows, e, top_k):
+    """Weights or scales of either projection: the expert's slots add nothing, on every way of
+    grouping the slots."""
+    layer = Layer(hip, 6, 320, 192, 17)
+    pick = np.arange(e) % 6
+    layer.gu, layer.dn = [layer.gu[i] for i in pick], [layer.dn[i] for i in pick]
+    layer.s1, layer.s2, layer.e = layer.s1[pick], layer.s2[pick], e
+    layer.tables(hip)
+    _, ids, w = layer.inputs(rows, top_k)
+    x = signs(layer.rng, rows, 320)
+    ids[:, 1:][ids[:, 1:] == 1] = 3
+    ids[:, 0] = 1
+    getattr(getattr(layer, table), field)[1] = 0
+    layer.gu[1] = layer.dn[1] = None
+    ref, terms = layer.oracle(x, ids, w)
+    assert_exact(layer.gu, codecs.bf16_bits_to_f64(x))
+    got = f64(_run(hip, layer, bf16_dev(x), ids, w))
+    assert np.all(np.abs(got - ref) <= bounds(ref, terms, 7.0)) and np.any(got)
