@@ -1033,8 +1033,9 @@ int launch_down(const FewArgs &p, void *stream) {
 }  // namespace
 
 extern "C" int64_t moe_few_workspace_bytes(int32_t rows, int32_t top_k, int32_t mi) {
-  if (rows <= 0 || top_k <= 0 || mi <= 0 || rows > kMaxRows ||
-      static_cast<int64_t>(rows) * top_k > kMaxIds)
+  if (rows <= 0 || top_k <= 0 || rows > kMaxRows ||
+      static_cast<int64_t>(rows) * top_k > kMaxIds || mi <= 0 || mi % 64 != 0 ||
+      mi > MOE_FEW_MAX_MI)
     return 0;
   return layout_of(static_cast<int64_t>(rows) * top_k, mi).bytes;
 }
