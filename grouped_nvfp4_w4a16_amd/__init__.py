@@ -974,7 +974,7 @@ def moe_rmsnorm_bf16(x, weight, y, eps: float = 1e-6, residual=None, h=None,
                      stream=None) -> None:
     """``h = bf16(x + residual)`` and ``y = bf16(h * weight / sqrt(mean(h^2) + eps))`` over BF16
     ``[rows, cols]`` views; ``h`` (the new residual stream, where given) may be ``x`` or
-    ``residual``, ``y`` may be ``x``."""
+    ``residual`` and ``y`` may be ``x``, but not one buffer for both."""
     shape, ld_x, ld_r, ld_h, ld_y = _norm_rows(x, weight, residual, h, y)
     rows, cols = shape
     if y is None:

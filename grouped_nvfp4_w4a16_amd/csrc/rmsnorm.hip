@@ -259,6 +259,14 @@ int check_norm(const char *name, const NormArgs &p, bool norm, int32_t rows) {
   MOE_REQUIRE((reinterpret_cast<uintptr_t>(p.q) & 7u) == 0 &&
                   (reinterpret_cast<uintptr_t>(p.scale) & 3u) == 0,
               "%s: q must be 8-byte aligned, scale 4-byte aligned", name);
+  MOE_REQUIRE(p.h == nullptr || p.h != p.y, "%s: h and y must not be the same buffer", name);
+  // In place: a row's output over that row's input, not over another row's.
+  const auto place_ok = [&](const void *out, int64_t ld, const void *in, int64_t ld_in) {
+    return rows == 1 || out == nullptr || out != in || ld == ld_in;
+  };
+  MOE_REQUIRE(place_ok(p.h, p.ld_h, p.x, p.ld_x) && place_ok(p.h, p.ld_h, p.res, p.ld_res) &&
+                  place_ok(p.y, p.ld_y, p.x, p.ld_x),
+              "%s: an output in place of an input needs its leading dimension", name);
   // A launch holds fewer than 2^32 threads.
   MOE_REQUIRE(rows < (1ll << 32) / kMaxThreads, "%s: at most 2^22 - 1 rows (got %d)", name, rows);
   return MOE_OK;

@@ -745,8 +745,9 @@ int moe_w8a8_grouped_gemm_swiglu(const uint8_t *a, int64_t lda, const float *a_s
  *   y         bf16 [rows, ld_y], or NULL in the quantised forms (not stored)   out
  *   q         E4M3 or INT8 codes [rows, ld_q]   out
  *   scale     float [rows, ld_scale] (E4M3), float [rows] (INT8)   out
- * h may be x or residual themselves (same pointer and leading dimension), y may be x; other
- * overlaps of outputs with inputs are not allowed.
+ * h may be x or residual themselves and y may be x (same pointer and leading dimension), but not
+ * one buffer for both. Other overlaps of outputs with inputs or with each other are not allowed
+ * (of equal pointers, h with y and another leading dimension in place are MOE_EINVAL).
  * Requirements (else MOE_EINVAL): 0 <= rows < 2^22; cols >= 0, a multiple of 8; eps finite and
  * >= 0; leading dimensions >= cols and multiples of 8; ld_scale >= ceil(cols / 128); x,
  * residual, weight, h and y 16-byte aligned, q 8-byte, scale 4-byte; required pointers
