@@ -1462,18 +1462,21 @@ def _layer_few(x, logits, bias, routed_scale, renormalize, topk_ids, topk_weight
     out, ld_out = _bf16_matrix(out, "out")
     if x.shape[1] != hidden or out.shape != x.shape:
         raise ValueError(f"x and out must be [{rows}, {hidden}]")
-    if isinstance(shared, (SharedExpert, SharedExpertInt8)):
-        term = shared.out
-    else:
-        term = shared
+    expert = isinstance(shared, (SharedExpert, SharedExpertInt8))
+    if shared is not None and not expert and getattr(shared, "dtype", None) is None:
+        raise TypeError("shared: expected a BF16 tensor, a SharedExpert or a SharedExpertInt8, got "
+                        f"{type(shared).__name__}")
+    term = shared.out if expert else shared
+    ld_s = 0
+    if term is not None:
+        ld_s = _bf16_matrix(term, "shared")[1]
+        if not expert and term.shape != x.shape:
+            raise ValueError(f"shared must be [{rows}, {hidden}]")
     handle = _launch_stream(stream, x, logits, bias, topk_ids, topk_weights, out, ws.buffer, term,
                             gate_up.packed_ptrs, down.packed_ptrs)  # before the first launch
-    if isinstance(shared, (SharedExpert, SharedExpertInt8)):
+    if expert:
         shared = shared(x, limit, stream) if isinstance(shared, SharedExpert) else \
             shared.for_combine(x, limit, stream)
-    ld_s = 0
-    if shared is not None:
-        shared, ld_s = _bf16_matrix(shared, "shared")
         if shared.shape != x.shape:
             raise ValueError(f"shared must be [{rows}, {hidden}]")
     if rows <= 1:
