@@ -1680,13 +1680,18 @@ class SharedExpertFp8:
 
 
 def moe_layer_fp8(x, topk_ids, topk_weights, gate_up: Fp8ExpertTable, down: Fp8ExpertTable,
-                  limit: float, ws: Fp8Workspace, out, shared=None, stream=None) -> None:
+                  limit: float, ws: Fp8Workspace, out, shared=None, stream=None,
+                  x_scale=None) -> None:
     """One routed MoE layer in FP8 over the BF16 rows of ``x``, in the order of moe_layer:
     align (and zero expert_out where experts are absent) -> quantise the rows -> grouped
     gate_up with the SwiGLU clamp and the quantisation of its output -> grouped down ->
     indexed combine into the BF16 ``out``. ``shared`` is the combine's shared term: a BF16
     ``[rows, H]`` tensor, a ``SharedPartials``, a ``SharedExpertFp8`` (run over the quantised
-    rows), or a ``SharedExpert`` or ``SharedExpertInt8`` (run over ``x``)."""
+    rows), or a ``SharedExpert`` or ``SharedExpertInt8`` (run over ``x``).
+    With ``x_scale`` (float32 ``[rows, ceil(H / 128)]``) ``x`` holds quantised rows instead, E4M3
+    codes as moe_rmsnorm_fp8 or moe_quant_fp8 leave them, and none is quantised here; a
+    ``SharedExpert`` or ``SharedExpertInt8``, which take BF16 rows, is refused then (run it before
+    and pass its output)."""
     _same_experts(gate_up, down)
     rows, top_k = topk_ids.shape
     hidden, mi = gate_up.k, gate_up.n // 2
@@ -1697,15 +1702,23 @@ def moe_layer_fp8(x, topk_ids, topk_weights, gate_up: Fp8ExpertTable, down: Fp8E
         raise ValueError("the workspace was made for other sizes")
     if tuple(x.shape) != (rows, hidden) or tuple(out.shape) != (rows, hidden):
         raise ValueError(f"x and out must be [{rows}, {hidden}]")
+    if x_scale is not None:
+        _fp8_matrix(x, "x")
+        _scale_matrix(x_scale, rows, _fp8_blocks(hidden), "x_scale")
+        if isinstance(shared, (SharedExpert, SharedExpertInt8)):
+            raise ValueError(f"shared: a {type(shared).__name__} takes BF16 rows, x is quantised")
     term = shared.partials if isinstance(shared, SharedPartials) else getattr(shared, "out", shared)
-    _launch_stream(stream, x, topk_ids, topk_weights, out, ws.x, gate_up.weight_ptrs,
+    _launch_stream(stream, x, x_scale, topk_ids, topk_weights, out, ws.x, gate_up.weight_ptrs,
                    down.weight_ptrs, term)  # before the first launch
     s = rows * top_k
     moe_align(topk_ids, gate_up.num_experts, ws.sorted_token_ids, ws.sorted_expert_ids,
               ws.expert_offsets, ws.token_to_perm, None, None, stream,
               zero=None if all(down.present) else ws.expert_out[:s])
-    xq, xs = ws.x[:rows], ws.x_scale[:rows]
-    moe_quant_fp8(x, xq, xs, stream)
+    if x_scale is None:
+        xq, xs = ws.x[:rows], ws.x_scale[:rows]
+        moe_quant_fp8(x, xq, xs, stream)
+    else:
+        xq, xs = x, x_scale
     act, act_scale = ws.act[:s], ws.act_scale[:s]
     moe_w8a8_grouped_gemm_swiglu(xq, xs, gate_up, ws.expert_offsets, act, act_scale, limit,
                                  ws.sorted_token_ids, stream=stream, workspace=ws.split)
