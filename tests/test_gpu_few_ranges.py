@@ -101,3 +101,20 @@ def test_an_expert_with_a_null_address_in_one_table(hip, table, field, rows, e, 
     assert_exact(layer.gu, codecs.bf16_bits_to_f64(x))
     got = f64(_run(hip, layer, bf16_dev(x), ids, w))
     assert np.all(np.abs(got - ref) <= bounds(ref, terms, 7.0)) and np.any(got)
+
+
+@pytest.mark.parametrize("rows,e,hidden,mi,top_k", [
+    (1, 3, 6144, 2048, 2), (3, 2, 8192, 256, 2), (8, 4, 2048, 768, 3), (16, 3, 4096, 448, 2),
+    (5, 3, 6208, 320, 3), (2, 5, 64, 2112, 4)])
+@pytest.mark.parametrize("limit", [7.0, 100.0])
+def test_wide_layers_whose_first_sums_are_exact(hip, rows, e, hidden, mi, top_k, limit):
+    """Real widths within bounds that a dropped channel or column does not pass
+    (test_few_check.py)."""
+    layer = Layer(hip, e, hidden, mi, rows + mi, mean=2.0)
+    _, ids, w = layer.inputs(rows, top_k)
+    x = signs(layer.rng, rows, hidden)
+    assert_exact(layer.gu, codecs.bf16_bits_to_f64(x))
+    ref, terms = layer.oracle(x, ids, w, limit)
+    got = f64(_run(hip, layer, bf16_dev(x), ids, w, limit))
+    elem = bounds(ref, terms, limit)
+    assert np.all(np.abs(got - ref) <= elem), float(np.max(np.abs(got - ref) / elem))
