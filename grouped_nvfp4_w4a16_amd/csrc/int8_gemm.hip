@@ -83,8 +83,8 @@ __device__ __forceinline__ float scaled(int sum, float sa, float sw) {
 // silu(min(g, L)) * clamp(u, -L, L), NaN kept by the IEEE minimum and maximum, in 15 operations (the
 // large tiles' epilogues are bound by them: 28 took 91 us where these take 87 at 4096 rows, width
 // 2048, K 6144). The rounding of the exponential's argument moves the result by |g| 2^-24 of
-// itself; below g = -88.7 the exponential of -g overflows and the result is 0 (it is below
-// 3e-37 L there).
+// itself; below g = -126 ln 2 = -87.34 the reciprocal leaves the normal numbers and the result is 0
+// (|silu| is below 1.03e-36 there).
 __device__ __forceinline__ float swiglu(float g, float u, float limit) {
   const float gc = __builtin_elementwise_minimum(g, limit);
   const float uc = __builtin_elementwise_maximum(__builtin_elementwise_minimum(u, limit), -limit);
