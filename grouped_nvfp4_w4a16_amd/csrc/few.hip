@@ -28,7 +28,7 @@
 //   - Kernel 2's activations differ by expert: they are staged through LDS per wave, at most
 //     kCap rows of an expert at a time (an expert with more is swept again).
 // Measured at 6144 x 2048, 8 of 256 experts a row: 43 us for 1 row (27 for its bytes at the rate of a
-// plain read), 76 for 2, 132 for 4, 214 to 228 for 8 (194), 398 for 16. The rest is:
+// plain read), 76 for 2, 132 for 4, 214 to 233 for 8 (194), 398 for 16. The rest is:
 //   - the starts of two kernels and the routing in each: the first weights are asked for 7 us into
 //     kernel 1 with 1 row and 12 with 8 (table entries and logits 2 to 5, grouping 1 to 3, the tokens'
 //     way through LDS 2), and 4 to 5 us into kernel 2;

@@ -18,10 +18,12 @@
 // What bounds it (256 CUs):
 //   - One row to some dozens: the weights from memory, the start of a block and of a launch: 6144 x
 //     2048 in 3.4 us of kernel (1 to 16 rows, weights in the last-level cache; 5.0 from memory).
-//   - Hundreds: what a CU takes in from its L2 (36 bytes a clock): 256 rows in 8.2 us.
+//   - Hundreds: what a CU takes in from its L2 (36 bytes a clock), each block all of K: 256 rows in
+//     8.1 to 9.0 us. (K in parts on several blocks is not built.)
 //   - Thousands: power. At 4096 x 6144 x 2048 the chip runs at 1.45 to 1.7 GHz of its 2.4; a step of
-//     the 192 x 256 tile takes 1980 clocks of which 1536 are products. 54 to 64 us by the
-//     codes' size (small codes toggle fewer bits), 1600 to 1900 TOPS; 8192^3 at 2200.
+//     the 192 x 256 tile takes 1980 clocks of which 1536 are products. 52 to 63 us by the codes
+//     (small ones toggle fewer bits) and by what the chip ran before, 1640 to 1980 TOPS; 8192^3 in
+//     419 to 441 us, 2490 to 2630.
 #include <algorithm>
 
 #include "buffer_io.h"
@@ -464,7 +466,9 @@ __global__ __launch_bounds__(C::kThreads, 2) void wide_kernel(GemmArgs p) {
 
     // The tile's outputs, 32 rows at a time through the wave's own piece of LDS, so that rows
     // leave in whole 64- to 192-byte pieces. Its 16-byte pieces are permuted within a row so that
-    // neither side meets a bank more often than it must.
+    // neither side meets a bank more often than it must. FP32 outputs (the shared expert's
+    // activations) go straight from the lanes, 16 bytes each: 109 us where BF16 ones take 105 in the
+    // same trace at 4096 rows, width 2048, K 6144.
     constexpr int kCols = kSwiglu ? 32 : 32 * NT;  // the wave's output columns
     constexpr int kOutRow = 2 * kCols, kLanes = kCols / 8;
     const auto place = [](int r, int piece) {

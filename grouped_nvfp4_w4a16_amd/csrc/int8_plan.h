@@ -24,11 +24,12 @@ enum Int8Tile {
 // A tile's shape and its estimate in microseconds: start + for every round of tiles over the
 // CUs, round + step x its steps of `slices` x 128 k (pair: of a round in which both blocks of a CU
 // have a tile). Fitted to the times of every tile at 260 random sizes (1 to 6000 rows, width and K
-// 128 to 8192). The tile with the least estimate is 1.2 % (plain) and 0.4 % (SwiGLU) slower than the
-// best of all, in the geometric mean, 1.15 times at worst; at 160 fresh sizes 0.8 and 0.4 %, 1.11
-// times. Without any one of the tiles the best of the others would be 0.1 to 7 % slower, up to 1.5
-// times at some size. (128 x 128 in pairs gains the plain form 0.03 %, 256 x 128 the SwiGLU form
-// nothing: they are not built.)
+// 128 to 8192). The tile with the least estimate is 1.2 % (plain) and 0.6 % (SwiGLU) slower than the
+// best of those built, in the geometric mean, 1.13 and 1.25 times at worst; at 300 fresh sizes 0.8
+// and 1.1 %, 1.12 and 1.30 times (SwiGLU of two tiles a CU: 128 x 128 taken where pairs are faster).
+// Without any one of the tiles the best of the others would be 0.1 to 7 % slower, up to 1.5 times at
+// some size. (128 x 128 in pairs gains the plain form 0.03 %, 256 x 128 the SwiGLU form nothing:
+// they are not built.)
 struct Int8Shape {
   int width, rows, slices;
   float start, round, step, pair;  // step 0: not built
